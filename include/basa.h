@@ -77,7 +77,8 @@ extern "C" {
 typedef enum basa_status {
   BASA_OK = 0,
   BASA_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad dtype value */
-  BASA_ERR_SHAPE = 2,       /* window or pool cell does not divide the grid */
+  BASA_ERR_SHAPE = 2,       /* window or pool cell does not divide the grid, or modulation
+                               rows do not divide the tokens */
   BASA_ERR_UNSUPPORTED = 3, /* head dim, window or box plan outside the bounds above */
   BASA_ERR_ALIGN = 4,       /* a pointer is not 16-byte aligned */
   BASA_ERR_WORKSPACE = 5,   /* workspace missing when global memory is requested */
@@ -310,6 +311,157 @@ BASA_API basa_status basa_full_attn(const void* q, const void* k, const void* v,
 BASA_API basa_status basa_window_attn_noalloc(const void* q, const void* k, const void* v,
                                               void* out, float* lse, const basa_params* p,
                                               cudaStream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Around the attention: the rows of a Diffusion Transformer block before and
+ * after it.  Every output is rounded once from fp32 arithmetic; sums run in a
+ * fixed order, so equal calls give equal bits.  Gradients of weights and
+ * modulations have the type of what they belong to.
+ * -------------------------------------------------------------------------- */
+
+/* Which elements of a head form a rotated pair j. */
+#define BASA_ROPE_PAIRS 0  /* (2j, 2j + 1) */
+#define BASA_ROPE_HALVES 1 /* (j, j + D/2), D = at + ah + aw the rotated width */
+
+/* RMS norm of q and k ahead of the rotation. */
+#define BASA_ROPE_NORM_NONE 0
+#define BASA_ROPE_NORM_HEAD 1  /* over the d values of each head; weights [d] */
+#define BASA_ROPE_NORM_TOKEN 2 /* over all heads of a token; weights [H * d], [Hkv * d] */
+
+typedef struct basa_rope_params {
+  int32_t B, H, Hkv;   /* batch, query heads, K/V heads (0 selects H; H a multiple of Hkv) */
+  int32_t T, Hg, Wg;   /* grid; L text tokens are the grid (1, 1, L) */
+  int32_t d;           /* head dim: 32, 64 or 128 */
+  int32_t at, ah, aw;  /* rotated elements of a head per axis: even, together at most d; the
+                          rest of the head is not rotated.  Pairs 0 .. at/2 - 1 turn with the
+                          time coordinate, the next ah/2 with the row, the next aw/2 with the
+                          column.  BASA_ROPE_HALVES needs at + ah + aw a multiple of 16. */
+  int32_t layout;      /* BASA_ROPE_PAIRS or BASA_ROPE_HALVES */
+  int32_t norm;        /* BASA_ROPE_NORM_*; _TOKEN takes H * d up to 16384 */
+  float eps;           /* of the norm: positive */
+  int32_t dtype;       /* basa_dtype of q, k, v and every gradient: BASA_F32 or BASA_BF16 */
+  int32_t out_dtype;   /* of q_out, k_out, v_out: dtype, or BASA_FP8_E4M3 (forward only) */
+  int32_t w_dtype;     /* of the norm weights and their gradients: BASA_F32 or BASA_BF16 */
+  float q_descale, k_descale, v_descale; /* e4m3 outputs: an element's value is its e4m3 value
+                          times this factor (0 selects 1), as basa_window_attn takes it; values
+                          beyond the type's largest are stored as the largest */
+  int64_t ldq, ldk, ldv;    /* elements from one token's row of q, k, v to the next: a multiple
+                          of 8 that holds the row; 0 selects dense rows.  So q, k, v may be
+                          slices of one projection output. */
+  int64_t ldgq, ldgk, ldgv; /* the same for dq, dk, dv */
+} basa_rope_params;
+
+/*
+ * The (cos, sin) pairs of every coordinate of the grid, fp32, in the order
+ * [T][at/2], [Hg][ah/2], [Wg][aw/2]: basa_rope_table_pairs(p) pairs.  Coordinate
+ * i of axis a stands at position start[a] + step[a] * i and pair j of the axis
+ * turns by position * theta^(-2j / width), width = at, ah or aw.  start and step
+ * are host arrays of three.  Angles are formed in fp64.  A program keeps the
+ * table for as long as the grid and positions stay the same; any other table of
+ * this layout (scaled or learned frequencies) serves as well.
+ */
+BASA_API int64_t basa_rope_table_pairs(const basa_rope_params* p);
+BASA_API basa_status basa_rope_table(float* table, double theta, const double* start,
+                                     const double* step, const basa_rope_params* p,
+                                     cudaStream_t stream);
+
+/*
+ * From a q/k/v projection to the attention's inputs: RMS norm of q and k
+ * (n = x / sqrt(mean(x^2) + eps) * weight), rotary positions with three axes
+ * (pair (a, b) becomes (a cos - b sin, a sin + b cos)), and v copied along.
+ * q, k, v: [B, T, Hg, Wg, H or Hkv, d] with dense heads and token rows ldq, ldk,
+ * ldv apart; q_out, k_out, v_out dense, as the attention calls take them.
+ * Weights may be NULL (ones), v and v_out both NULL, table NULL when nothing is
+ * rotated.  An output may be its own input (same address, dense rows, same
+ * type); other overlap is not allowed.  One launch.
+ */
+BASA_API basa_status basa_qkv_rope(const void* q, const void* k, const void* v,
+                                   const void* q_weight, const void* k_weight, const float* table,
+                                   void* q_out, void* k_out, void* v_out,
+                                   const basa_rope_params* p, cudaStream_t stream);
+
+/*
+ * Backward of basa_qkv_rope: dq, dk, dv and the weights' gradients, from the
+ * gradients dq_out, dk_out, dv_out of its outputs (dense, e.g. from
+ * basa_window_attn_bwd) and its inputs q, k (which the call without a norm does
+ * not read: they may be NULL).  dq, dk, dv have token rows ldgq, ldgk, ldgv
+ * apart, so they may be slices of one buffer.  dv_out and dv may both be NULL,
+ * and a weight's gradient NULL when it is not wanted.  workspace:
+ * basa_qkv_rope_bwd_workspace_size(p) bytes (asked with the device of the call
+ * current), 16-byte aligned, needed for the weights' gradients only.  dq may be
+ * dq_out (and so on) where the rows are dense.
+ */
+BASA_API size_t basa_qkv_rope_bwd_workspace_size(const basa_rope_params* p);
+BASA_API basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,
+                                       const void* q, const void* k, const void* q_weight,
+                                       const void* k_weight, const float* table, void* dq,
+                                       void* dk, void* dv, void* dq_weight, void* dk_weight,
+                                       void* workspace, const basa_rope_params* p,
+                                       cudaStream_t stream);
+
+/* Norms of a row of C values: (z - mean) / sqrt(var + eps), z / sqrt(mean(z^2) + eps). */
+#define BASA_NORM_NONE 0
+#define BASA_NORM_LAYER 1
+#define BASA_NORM_RMS 2
+
+typedef struct basa_gnorm_params {
+  int64_t rows;       /* tokens of all samples */
+  int64_t groups;     /* modulation rows, >= 1; rows must be a multiple: rows / groups
+                         consecutive tokens share one (groups = 1: all, B: a sample's, B * T: a
+                         frame's, rows: each token its own) */
+  int32_t C;          /* width: a multiple of 8, at most 8192 */
+  int32_t norm;       /* of the sum, ahead of the next block: BASA_NORM_* */
+  int32_t post_norm;  /* of the branch: BASA_NORM_* */
+  float eps, post_eps;/* positive where there is a norm */
+  float res_scale;    /* factor on the residual stream; finite */
+  int32_t x_dtype;    /* of x, x_out and their gradients: BASA_F32 or BASA_BF16 */
+  int32_t dtype;      /* of y, h and their gradients: x_dtype, or BASA_BF16 beside fp32 x */
+  int32_t mod_dtype;  /* of gate, scale, shift and their gradients */
+  int32_t w_dtype;    /* of weight, bias, post_weight and their gradients */
+  int64_t ld_gate, ld_scale, ld_shift; /* elements from one modulation row to the next, a
+                         multiple of 8 (slices of one modulation output); 0: one row for all */
+} basa_gnorm_params;
+
+/*
+ * The border between two blocks: the branch y joins the residual stream x
+ * through its own norm, its gate and the residual scale, and the sum is
+ * normalised and modulated for the next block,
+ *   x_out = res_scale * x + gate * (post_norm(y) * post_weight)
+ *   h     = (norm(x_out) * weight + bias) * (1 + scale) + shift.
+ * x, y, x_out, h: dense [rows, C]; gate, scale, shift: groups rows of C; weight,
+ * bias, post_weight: [C].  NULL leaves a factor or summand out.  y = NULL (then
+ * x_out, gate and a post-norm are not allowed): h of x alone.  norm =
+ * BASA_NORM_NONE (then h, weight, bias, scale, shift must be NULL): x_out alone.
+ * h is taken from the sum before it is rounded to x_dtype.  stats (may be NULL)
+ * receives fp32 [rows, 4]: mean and 1/deviation of the norm, then of the
+ * post-norm, zeros where there is none.  x_out may be x, and h may be y; other
+ * overlap is not allowed.  One launch.
+ */
+BASA_API basa_status basa_gated_norm(const void* x, const void* y, const void* gate,
+                                     const void* post_weight, const void* weight,
+                                     const void* bias, const void* scale, const void* shift,
+                                     void* x_out, void* h, float* stats,
+                                     const basa_gnorm_params* p, cudaStream_t stream);
+
+/*
+ * Backward of basa_gated_norm from the gradients dh and dx_out of its outputs
+ * (dx_out NULL: zero; dh only with a norm), its output x_out, stats, and y (NULL
+ * where neither dgate nor a post-norm needs it).  Without a norm x_out may be
+ * NULL, and so may stats without any.  dy NULL: the call had no branch.  dgate,
+ * dscale, dshift: dense [groups, C]; they, dweight, dbias, dpost_weight [C] are
+ * NULL when not wanted.  workspace: basa_gated_norm_bwd_workspace_size(p) bytes
+ * (asked with the device of the call current), 16-byte aligned, needed for these
+ * sums only.  dx may be dx_out; other overlap is not allowed.
+ */
+BASA_API size_t basa_gated_norm_bwd_workspace_size(const basa_gnorm_params* p);
+BASA_API basa_status basa_gated_norm_bwd(const void* dh, const void* x_out, const float* stats,
+                                         const void* y, const void* dx_out, const void* gate,
+                                         const void* post_weight, const void* weight,
+                                         const void* bias, const void* scale, void* dx, void* dy,
+                                         void* dgate, void* dpost_weight, void* dweight,
+                                         void* dbias, void* dscale, void* dshift,
+                                         void* workspace, const basa_gnorm_params* p,
+                                         cudaStream_t stream);
 
 /*
  * Test and diagnostics only: synchronises `stream`, then reports and clears the

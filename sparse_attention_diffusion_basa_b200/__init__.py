@@ -19,11 +19,14 @@ import torch
 from . import _lib
 from ._lib import BasaError, BasaParams, BASA_F32, BASA_BF16, BASA_FP8_E4M3  # noqa: F401
 from ._lib import BASA_FLAG_PAD_GRID, BASA_FLAG_BWD_CUDA_CORES  # noqa: F401
+from .block import (GatedNormGrads, gated_norm, gated_norm_bwd, qkv_rope,  # noqa: F401
+                    qkv_rope_bwd, rope_table)
 
 __all__ = ["window_attn", "window_attn_gm", "full_attn", "joint_attn", "window_attn_bwd",
            "joint_attn_bwd",
            "pool_kv", "workspace_size", "bwd_workspace_size", "joint_workspace_size",
            "joint_bwd_workspace_size", "get_status", "window_tiles", "make_params", "BasaError",
+           "rope_table", "qkv_rope", "qkv_rope_bwd", "gated_norm", "gated_norm_bwd", "GatedNormGrads",
            "library_path", "BASA_FLAG_PAD_GRID", "BASA_FLAG_BWD_CUDA_CORES"]
 
 library_path = _lib.LIB_PATH

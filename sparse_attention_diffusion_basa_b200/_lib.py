@@ -20,13 +20,19 @@ BASA_F32, BASA_BF16, BASA_FP8_E4M3 = 0, 1, 2
 BASA_FLAG_TEST_WITHHOLD_LOADS = 0x1
 BASA_FLAG_BWD_CUDA_CORES = 0x2
 BASA_FLAG_PAD_GRID = 0x4
+BASA_ROPE_LAYOUT = {"pairs": 0, "halves": 1}
+BASA_ROPE_NORM = {None: 0, "head": 1, "token": 2}
+BASA_NORM = {None: 0, "layer": 1, "rms": 2}
 
 # Every symbol include/basa.h declares.
 EXPORTS = ("basa_status_string", "basa_version", "basa_workspace_size", "basa_pool_kv",
            "basa_window_attn", "basa_window_attn_gm", "basa_full_attn", "basa_get_status",
            "basa_window_tiles", "basa_window_attn_noalloc",
            "basa_joint_attn", "basa_window_attn_bwd", "basa_bwd_workspace_size",
-           "basa_joint_workspace_size", "basa_joint_attn_bwd", "basa_joint_bwd_workspace_size")
+           "basa_joint_workspace_size", "basa_joint_attn_bwd", "basa_joint_bwd_workspace_size",
+           "basa_rope_table_pairs", "basa_rope_table", "basa_qkv_rope", "basa_qkv_rope_bwd",
+           "basa_qkv_rope_bwd_workspace_size", "basa_gated_norm", "basa_gated_norm_bwd",
+           "basa_gated_norm_bwd_workspace_size")
 
 
 class BasaParams(ctypes.Structure):
@@ -37,6 +43,23 @@ class BasaParams(ctypes.Structure):
         ("wait_timeout_ms", ctypes.c_uint32), ("Hkv", ctypes.c_int32),
         ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float),
         ("v_descale", ctypes.c_float)]
+
+
+class BasaRopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "H", "Hkv", "T", "Hg", "Wg", "d", "at", "ah", "aw", "layout", "norm")] + [
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("w_dtype", ctypes.c_int32), ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float),
+        ("v_descale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "ldgq", "ldgk", "ldgv")]
+
+
+class BasaGnormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("C", "norm", "post_norm")] + [
+        (n, ctypes.c_float) for n in ("eps", "post_eps", "res_scale")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "dtype", "mod_dtype", "w_dtype")] + [
+        (n, ctypes.c_int64) for n in ("ld_gate", "ld_scale", "ld_shift")]
 
 
 class BasaError(RuntimeError):
@@ -95,6 +118,23 @@ def load():
     lib.basa_window_tiles.restype = ctypes.c_int
     lib.basa_window_attn_noalloc.argtypes = [vp, vp, vp, vp, vp, P, vp]
     lib.basa_window_attn_noalloc.restype = ctypes.c_int
+    R, G, f64 = ctypes.POINTER(BasaRopeParams), ctypes.POINTER(BasaGnormParams), ctypes.c_double
+    lib.basa_rope_table_pairs.argtypes = [R]
+    lib.basa_rope_table_pairs.restype = ctypes.c_int64
+    lib.basa_rope_table.argtypes = [vp, f64, ctypes.POINTER(f64), ctypes.POINTER(f64), R, vp]
+    lib.basa_rope_table.restype = ctypes.c_int
+    lib.basa_qkv_rope.argtypes = [vp] * 9 + [R, vp]
+    lib.basa_qkv_rope.restype = ctypes.c_int
+    lib.basa_qkv_rope_bwd.argtypes = [vp] * 14 + [R, vp]
+    lib.basa_qkv_rope_bwd.restype = ctypes.c_int
+    lib.basa_qkv_rope_bwd_workspace_size.argtypes = [R]
+    lib.basa_qkv_rope_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.basa_gated_norm.argtypes = [vp] * 11 + [G, vp]
+    lib.basa_gated_norm.restype = ctypes.c_int
+    lib.basa_gated_norm_bwd.argtypes = [vp] * 19 + [G, vp]
+    lib.basa_gated_norm_bwd.restype = ctypes.c_int
+    lib.basa_gated_norm_bwd_workspace_size.argtypes = [G]
+    lib.basa_gated_norm_bwd_workspace_size.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
