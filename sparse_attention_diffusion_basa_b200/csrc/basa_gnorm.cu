@@ -47,139 +47,101 @@ struct GnArgs {
   int need_y;
 };
 
-// ---------------------------------------------------------------------------
-// Read-ahead ring.  Every thread copies its own columns to its own bytes of a
-// stage and is the only one to read them, so the ring needs no barrier.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// Waits until at most depth - 1 of this thread's groups are in flight.
-__device__ __forceinline__ void copy_wait(int depth) {
+// Waits until at most depth - 1 of this thread's copies are in flight.
+__device__ __forceinline__ void ring_wait(int depth) {
   if (depth == 3)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    copy_wait<2>();
   else if (depth == 2)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    copy_wait<1>();
   else
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    copy_wait<0>();
 }
-
-// A thread's vectors of one row of one tensor in a stage: 16-byte pieces, the
-// threads of a warp side by side.
 template <typename T>
-struct Slot {
-  static constexpr int kPieces = (int)sizeof(T) / 2;
-  __device__ static __forceinline__ void fetch(char* at, const void* row, int j, int col,
-                                               int threads) {
-    const char* src = static_cast<const char*>(row) + (size_t)col * sizeof(T);
-    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(at)) +
-                         (uint32_t)((j * kPieces * threads + (int)threadIdx.x) * 16);
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) copy16(dst + p * threads * 16, src + p * 16);
-  }
-  __device__ static __forceinline__ void take(const char* at, int j, int threads, float (&f)[8]) {
-    const uint4* s = reinterpret_cast<const uint4*>(at) + j * kPieces * threads + threadIdx.x;
-    Raw8<T> r;
-    r.a = s[0];
-    if constexpr (kPieces == 2) r.b = s[threads];
-    widen8(r, f);
-  }
-};
-
-template <typename T>
-__host__ __device__ constexpr int slot_bytes(int kv, int threads) {
-  return kv * threads * 8 * (int)sizeof(T);
+__device__ __forceinline__ void take(const char* at, int j, f2 (&f)[4]) {
+  Raw8<T> r;
+  Slot<T>::take(at, j, blockDim.x, threadIdx.x, r);
+  widen8(r, f);
 }
 
 // ---------------------------------------------------------------------------
-// Sums over a row
+// Sums over a row.  Every warp leaves its part in shared memory and, behind one
+// barrier, adds up all warps' parts itself, one a lane.  `buf` alternates from
+// sum to sum, so that barrier is the only one.
 // ---------------------------------------------------------------------------
 struct RowSmem {
   float2 red[2][kMaxWarps];
-  float cnt[kMaxWarps];     // elements of a warp
 };
 
-__device__ __forceinline__ float2 row_sum2(float a, float b, RowSmem& sm, int& buf) {
-  a = lane_sum<32>(a);
-  b = lane_sum<32>(b);
-  if ((threadIdx.x & 31) == 0) sm.red[buf][threadIdx.x >> 5] = make_float2(a, b);
+__device__ __forceinline__ float2 share(float2 v, RowSmem& sm, int& buf) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sm.red[buf][threadIdx.x >> 5] = v;
   __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
-    const float2 v = sm.red[buf][i];
-    s.x += v.x;
-    s.y += v.y;
-  }
+  v = lane < (int)(blockDim.x >> 5) ? sm.red[buf][lane] : make_float2(0.f, 0.f);
   buf ^= 1;
-  return s;
+  return v;
 }
 
-// (mean, rstd) of a row held kV * 8 values a thread.  Layer: the squares are
-// taken about each warp's own mean and joined about the row's (Chan, Golub and
-// LeVeque's update), so a mean far from zero costs no digits and one barrier is
-// enough.
+__device__ __forceinline__ float2 row_sum2(f2 a, f2 b, RowSmem& sm, int& buf) {
+  const float2 v = lane_sum<32>(make_float2(sum2(a), sum2(b)));
+  return lane_sum<32>(share(v, sm, buf));
+}
+
+// Elements of a row that warp i holds.
+__device__ __forceinline__ float warp_elements(int i, int kv, int nvec) {
+  int n = 0;
+  for (int j = 0; j < kv; ++j) {
+    const int left = nvec - j * (int)blockDim.x - 32 * i;
+    n += left < 0 ? 0 : left > 32 ? 32 : left;
+  }
+  return (float)(8 * n);
+}
+
+struct Counts {      // elements of a warp: of this thread's, and of warp number `lane`
+  float inv_mine;    // 1 / elements, 0 where there are none
+  float lanes, inv_lanes;
+};
+
+// (mean, rstd) of a row held kV * 8 values a thread, zeros where ok is false.
+// Layer: the squares are taken about each warp's own mean and joined about the
+// row's (Chan, Golub and LeVeque's update), so a mean far from zero costs no
+// digits and one barrier is enough.
 template <int kV>
-__device__ __forceinline__ float2 row_stats(const float (&f)[kV][8], const bool (&ok)[kV],
-                                            int kind, float eps, float inv, RowSmem& sm,
+__device__ __forceinline__ float2 row_stats(const f2 (&f)[kV][4], const bool (&ok)[kV], int kind,
+                                            float eps, float inv, const Counts& n, RowSmem& sm,
                                             int& buf) {
-  const int warp = threadIdx.x >> 5;
-  float s = 0.f, q = 0.f;
+  f2 q = pk(0.f, 0.f);
   if (kind == BASA_NORM_LAYER) {
+    f2 t = pk(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t = add2(t, f[j][i]);
+    const float s = lane_sum<32>(sum2(t));
+    const float m = -s * n.inv_mine;
+    const f2 mm = pk(m, m);
 #pragma unroll
     for (int j = 0; j < kV; ++j)
       if (ok[j])
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += f[j][i];
-    s = lane_sum<32>(s);
-    const float m = s / fmaxf(sm.cnt[warp], 1.f);
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-      if (ok[j])
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(f[j][i] - m, f[j][i] - m, q);
-    q = lane_sum<32>(q);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-      if (ok[j])
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(f[j][i], f[j][i], q);
-    q = lane_sum<32>(q);
+        for (int i = 0; i < 4; ++i) {
+          const f2 d = add2(f[j][i], mm);
+          q = fma2(d, d, q);
+        }
+    const float2 v = share(make_float2(s, lane_sum<32>(sum2(q))), sm, buf);
+    const float mean = lane_sum<32>(v.x) * inv;
+    const float d = v.x * n.inv_lanes - mean;
+    const float m2 = lane_sum<32>(fmaf(n.lanes * d, d, v.y));
+    return make_float2(mean, rsqrtf(m2 * inv + eps));
   }
-  if ((threadIdx.x & 31) == 0) sm.red[buf][warp] = make_float2(s, q);
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-  float mean = 0.f, m2 = 0.f;
-  if (kind == BASA_NORM_LAYER) {
-    for (int i = 0; i < warps; ++i) mean += sm.red[buf][i].x;
-    mean *= inv;
-    for (int i = 0; i < warps; ++i) {
-      const float n = sm.cnt[i];
-      const float d = sm.red[buf][i].x / fmaxf(n, 1.f) - mean;
-      m2 += sm.red[buf][i].y + n * d * d;
-    }
-  } else {
-    for (int i = 0; i < warps; ++i) m2 += sm.red[buf][i].y;
-  }
-  buf ^= 1;
-  return make_float2(mean, rsqrtf(m2 * inv + eps));
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q = fma2(f[j][i], f[j][i], q);
+  const float2 v = share(make_float2(0.f, lane_sum<32>(sum2(q))), sm, buf);
+  return make_float2(0.f, rsqrtf(lane_sum<32>(v.y) * inv + eps));
 }
 
-__device__ __forceinline__ void count_elements(RowSmem& sm, int kv, int nvec) {
-  const int threads = blockDim.x;
-  if ((int)threadIdx.x < threads / 32) {
-    int n = 0;
-    for (int j = 0; j < kv; ++j) {
-      const int left = nvec - j * threads - 32 * (int)threadIdx.x;
-      n += left < 0 ? 0 : left > 32 ? 32 : left;
-    }
-    sm.cnt[threadIdx.x] = (float)(8 * n);
-  }
-  __syncthreads();
-}
+__device__ __forceinline__ f2 both(float v) { return pk(v, v); }
 
 // ---------------------------------------------------------------------------
 // Forward
@@ -189,52 +151,62 @@ __global__ void __launch_bounds__(kThreads, kCtas) gnorm_kernel(GnArgs a) {
   extern __shared__ __align__(16) char ring[];
   __shared__ RowSmem sm;
   const int tid = threadIdx.x, threads = blockDim.x, nvec = a.C / 8;
-  int col[kV];
   bool ok[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    ok[j] = j * threads + tid < nvec;
-    col[j] = (j * threads + tid) * 8;
+  for (int j = 0; j < kV; ++j) ok[j] = j * threads + tid < nvec;
+  const int next = threads * 8;  // columns from one of a thread's vectors to the next
+  Counts cnt;
+  {
+    const float mine = warp_elements(tid >> 5, kV, nvec);
+    cnt.inv_mine = mine > 0.f ? 1.f / mine : 0.f;
+    cnt.lanes = (tid & 31) < (threads >> 5) ? warp_elements(tid & 31, kV, nvec) : 0.f;
+    cnt.inv_lanes = cnt.lanes > 0.f ? 1.f / cnt.lanes : 0.f;
   }
-  count_elements(sm, kV, nvec);
-  const int x_bytes = slot_bytes<TX>(kV, threads);
-  const int stage = x_bytes + (kBranch ? slot_bytes<TY>(kV, threads) : 0);
-  const long long r0 = a.rows * blockIdx.x / gridDim.x;
-  const long long r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
-  int to_stage = 0;
-  auto fetch = [&](long long r) {
-    if (r < r1) {
-      char* at = ring + to_stage * stage;
+  const int x_bytes = Slot<TX>::bytes(kV, threads);
+  const int stage = x_bytes + (kBranch ? Slot<TY>::bytes(kV, threads) : 0);
+  const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
+  const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
+  const long long off = (long long)r0 * a.C + tid * 8;
+  const TX* x = static_cast<const TX*>(a.x) + off;
+  const TY* y = kBranch ? static_cast<const TY*>(a.y) + off : nullptr;
+  TX* xo = kBranch ? static_cast<TX*>(a.xo) + off : nullptr;
+  TY* h = kNorm ? static_cast<TY*>(a.h) + off : nullptr;
+  const uint32_t ring_at = shared_u32(ring);
+  int ahead = 0, to_stage = 0;  // rows asked for, and the stage of the next
+  auto fetch = [&]() {
+    if (r0 + ahead < r1) {
+      const uint32_t at = ring_at + to_stage;
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
-          Slot<TX>::fetch(at, static_cast<const TX*>(a.x) + r * a.C, j, col[j], threads);
-          if (kBranch)
-            Slot<TY>::fetch(at + x_bytes, static_cast<const TY*>(a.y) + r * a.C, j, col[j],
-                            threads);
+          Slot<TX>::fetch(at, x + j * next, j, threads, tid);
+          if (kBranch) Slot<TY>::fetch(at + x_bytes, y + j * next, j, threads, tid);
         }
+      x += a.C;
+      if (kBranch) y += a.C;
     }
     copy_commit();
-    to_stage = to_stage + 1 == a.depth ? 0 : to_stage + 1;
+    ++ahead;
+    to_stage = to_stage + stage == a.depth * stage ? 0 : to_stage + stage;
   };
-  for (int s = 0; s < a.depth - 1; ++s) fetch(r0 + s);
-  float G[kV][8], S[kV][8], B[kV][8];
+  for (int s = 0; s < a.depth - 1; ++s) fetch();
+  f2 G[kV][4], S[kV][4], B[kV][4];
   long long g_end = r0;
   int buf = 0, at_stage = 0;
-  for (long long r = r0; r < r1; ++r) {
-    fetch(r + a.depth - 1);
+  for (int r = r0; r < r1; ++r) {
+    fetch();
     if (r >= g_end) {  // another modulation row
       const long long g = r / a.group;
       g_end = (g + 1) * a.group;
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        const long long c = ok[j] ? col[j] : 0;
-        float p[8], q[8];
+        const long long c = ok[j] ? tid * 8 + j * next : 0;
+        f2 p[4], q[4];
         if (kBranch) {
           param8(a.gate, a.mod_bf16, g * a.ld_gate + c, 1.f, G[j]);
           param8(a.pw, a.w_bf16, c, 1.f, p);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) G[j][i] *= p[i];
+          for (int i = 0; i < 4; ++i) G[j][i] = mul2(G[j][i], p[i]);
         }
         if (kNorm) {
           param8(a.scale, a.mod_bf16, g * a.ld_scale + c, 0.f, p);
@@ -242,53 +214,66 @@ __global__ void __launch_bounds__(kThreads, kCtas) gnorm_kernel(GnArgs a) {
           param8(a.b, a.w_bf16, c, 0.f, B[j]);
           param8(a.shift, a.mod_bf16, g * a.ld_shift + c, 0.f, q);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            S[j][i] *= 1.f + p[i];
-            B[j][i] = fmaf(B[j][i], 1.f + p[i], q[i]);
+          for (int i = 0; i < 4; ++i) {
+            p[i] = add2(p[i], both(1.f));
+            S[j][i] = mul2(S[j][i], p[i]);
+            B[j][i] = fma2(B[j][i], p[i], q[i]);
           }
         }
       }
     }
-    copy_wait(a.depth);
-    const char* at = ring + at_stage * stage;
-    at_stage = at_stage + 1 == a.depth ? 0 : at_stage + 1;
-    float f[kV][8];
+    ring_wait(a.depth);
+    const char* at = ring + at_stage;
+    at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
+    f2 f[kV][4];
     float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
-    if (kBranch) {
-      float y[kV][8];
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) Slot<TY>::take(at + x_bytes, j, threads, y[j]);
-      float m = 0.f, s = 1.f;
-      if (a.post != BASA_NORM_NONE) {
-        post = row_stats<kV>(y, ok, a.post, a.post_eps, a.inv, sm, buf);
-        m = post.x;
-        s = post.y;
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[j][i] = 0;
+    if (kBranch) {
+      f2 u[kV][4];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[j][i] = 0;
+        if (ok[j]) take<TY>(at + x_bytes, j, u[j]);
       }
+      if (a.post != BASA_NORM_NONE) {
+        post = row_stats<kV>(u, ok, a.post, a.post_eps, a.inv, cnt, sm, buf);
+        const f2 m = both(-post.x), s = both(post.y);
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[j][i] = mul2(add2(u[j][i], m), s);
+      }
+      const f2 res = both(a.res);
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
-          Slot<TX>::take(at, j, threads, f[j]);
+          take<TX>(at, j, f[j]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            f[j][i] = fmaf(a.res, f[j][i], (y[j][i] - m) * s * G[j][i]);
-          store8(static_cast<TX*>(a.xo) + r * a.C + col[j], f[j]);
+          for (int i = 0; i < 4; ++i) f[j][i] = fma2(res, f[j][i], mul2(u[j][i], G[j][i]));
+          store8(xo + j * next, f[j]);
         }
+      xo += a.C;
     } else {
 #pragma unroll
       for (int j = 0; j < kV; ++j)
-        if (ok[j]) Slot<TX>::take(at, j, threads, f[j]);
+        if (ok[j]) take<TX>(at, j, f[j]);
     }
     if (kNorm) {
-      pre = row_stats<kV>(f, ok, a.norm, a.eps, a.inv, sm, buf);
+      pre = row_stats<kV>(f, ok, a.norm, a.eps, a.inv, cnt, sm, buf);
+      const f2 m = both(-pre.x), s = both(pre.y);
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            f[j][i] = fmaf((f[j][i] - pre.x) * pre.y, S[j][i], B[j][i]);
-          store8(static_cast<TY*>(a.h) + r * a.C + col[j], f[j]);
+          for (int i = 0; i < 4; ++i)
+            f[j][i] = fma2(mul2(add2(f[j][i], m), s), S[j][i], B[j][i]);
+          store8(h + j * next, f[j]);
         }
+      h += a.C;
     }
     if (a.stats && tid == 0) a.stats[r] = make_float4(pre.x, pre.y, post.x, post.y);
   }
@@ -297,225 +282,248 @@ __global__ void __launch_bounds__(kThreads, kCtas) gnorm_kernel(GnArgs a) {
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
+template <int kV>
+struct ColSums {
+  f2 a[kV][4], s[kV][4], d[kV][4];  // gh xh, gh, t yh
+};
+
+// The sums of modulation row g end: into the result where all its rows lay in
+// this CTA's range, into the CTA's partial rows otherwise; and, times the
+// modulation, into the CTA's partial rows of the weights.
+template <int kV, bool kBranch, bool kNorm>
+__device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, long long g, bool whole,
+                                   bool first, bool again) {
+  float* pg = a.part_g + ((long long)blockIdx.x * 2 + (first ? 0 : 1)) * 3 * a.C;
+  float* pw = a.part_w + (long long)blockIdx.x * 3 * a.C;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
+    if (col >= a.C) continue;
+    f2 v[4], p[4], q[4];
+    if (a.part_w) {
+      auto add = [&](float* to, const f2(&sum)[4]) {
+        f2 old[4];
+        if (again) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 o = *reinterpret_cast<const float2*>(to + 2 * i);
+            old[i] = pk(o.x, o.y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = again ? fma2(p[i], sum[i], old[i]) : mul2(p[i], sum[i]);
+        store8(to, v);
+      };
+      if (kNorm) {
+        param8(a.scale, a.mod_bf16, g * a.ld_scale + col, 0.f, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = add2(p[i], both(1.f));
+        add(pw + col, c.a[j]);
+        add(pw + a.C + col, c.s[j]);
+      }
+      if (kBranch) {
+        param8(a.gate, a.mod_bf16, g * a.ld_gate + col, 1.f, p);
+        add(pw + 2 * a.C + col, c.d[j]);
+      }
+    }
+    if (whole) {
+      if (kNorm && a.dscale) {
+        param8(a.w, a.w_bf16, col, 1.f, p);
+        param8(a.b, a.w_bf16, col, 0.f, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fma2(p[i], c.a[j][i], mul2(q[i], c.s[j][i]));
+        store_param8(a.dscale, a.mod_bf16, g * a.C + col, v);
+      }
+      if (kNorm && a.dshift) store_param8(a.dshift, a.mod_bf16, g * a.C + col, c.s[j]);
+      if (kBranch && a.dgate) {
+        param8(a.pw, a.w_bf16, col, 1.f, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(p[i], c.d[j][i]);
+        store_param8(a.dgate, a.mod_bf16, g * a.C + col, v);
+      }
+    } else if (a.part_g) {
+      if (kNorm) {
+        store8(pg + col, c.a[j]);
+        store8(pg + a.C + col, c.s[j]);
+      }
+      if (kBranch) store8(pg + 2 * a.C + col, c.d[j]);
+    }
+  }
+}
+
 template <typename TX, typename TY, int kV, int kThreads, bool kBranch, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 1) gnorm_bwd_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) gnorm_bwd_kernel(const __grid_constant__ GnArgs a) {
   extern __shared__ __align__(16) char ring[];
   __shared__ RowSmem sm;
   const int tid = threadIdx.x, threads = blockDim.x, nvec = a.C / 8;
-  int col[kV];
   bool ok[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    ok[j] = j * threads + tid < nvec;
-    col[j] = (j * threads + tid) * 8;
-  }
-  const int xb = slot_bytes<TX>(kV, threads), yb = slot_bytes<TY>(kV, threads);
-  const int o_gx = 0, o_y = o_gx + (a.gx ? xb : 0), o_x = o_y + (a.need_y ? yb : 0),
-            o_gh = o_x + xb;
+  for (int j = 0; j < kV; ++j) ok[j] = j * threads + tid < nvec;
+  const int next = threads * 8;
+  const int xb = Slot<TX>::bytes(kV, threads), yb = Slot<TY>::bytes(kV, threads);
+  const int o_y = a.gx ? xb : 0, o_x = o_y + (a.need_y ? yb : 0), o_gh = o_x + xb;
   const int stage = kNorm ? o_gh + yb : o_x;
-  const long long r0 = a.rows * blockIdx.x / gridDim.x;
-  const long long r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
-  int to_stage = 0;
-  auto fetch = [&](long long r) {
-    if (r < r1) {
-      char* at = ring + to_stage * stage;
+  const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
+  const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
+  long long from = (long long)r0 * a.C + tid * 8, to = from;  // of the next row read, written
+  const uint32_t ring_at = shared_u32(ring);
+  int ahead = 0, to_stage = 0;
+  auto fetch = [&]() {
+    if (r0 + ahead < r1) {
+      const uint32_t at = ring_at + to_stage;
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
+          const long long e = from + j * next;
           if (kNorm) {
-            Slot<TX>::fetch(at + o_x, static_cast<const TX*>(a.x) + r * a.C, j, col[j], threads);
-            Slot<TY>::fetch(at + o_gh, static_cast<const TY*>(a.gh) + r * a.C, j, col[j], threads);
+            Slot<TX>::fetch(at + o_x, static_cast<const TX*>(a.x) + e, j, threads, tid);
+            Slot<TY>::fetch(at + o_gh, static_cast<const TY*>(a.gh) + e, j, threads, tid);
           }
-          if (a.gx)
-            Slot<TX>::fetch(at + o_gx, static_cast<const TX*>(a.gx) + r * a.C, j, col[j], threads);
+          if (a.gx) Slot<TX>::fetch(at, static_cast<const TX*>(a.gx) + e, j, threads, tid);
           if (kBranch && a.need_y)
-            Slot<TY>::fetch(at + o_y, static_cast<const TY*>(a.y) + r * a.C, j, col[j], threads);
+            Slot<TY>::fetch(at + o_y, static_cast<const TY*>(a.y) + e, j, threads, tid);
         }
+      from += a.C;
     }
     copy_commit();
-    to_stage = to_stage + 1 == a.depth ? 0 : to_stage + 1;
+    ++ahead;
+    to_stage = to_stage + stage == a.depth * stage ? 0 : to_stage + stage;
   };
-  for (int s = 0; s < a.depth - 1; ++s) fetch(r0 + s);
-  float G[kV][8], S[kV][8];                    // gate * pw, (1 + scale) * w
-  float sa[kV][8], ss[kV][8], sd[kV][8];       // sums of gh xh, gh, t yh
+  for (int s = 0; s < a.depth - 1; ++s) fetch();
+  f2 G[kV][4], S[kV][4];  // gate * pw, (1 + scale) * w
+  ColSums<kV> sum;
   long long g = r0 / a.group, g_end = r0;
   const long long g_first = g;
   bool flushed = false;
-  // the sums of modulation row g end here
-  auto flush = [&](long long end) {
-    const bool whole = g * a.group >= r0 && (g + 1) * a.group <= end;
-    float* pg = a.part_g + ((long long)blockIdx.x * 2 + (g != g_first)) * 3 * a.C;
-    float* pw = a.part_w + (long long)blockIdx.x * 3 * a.C;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      if (!ok[j]) continue;
-      const int c = col[j];
-      float v[8], p[8], q[8];
-      if (a.part_w) {
-        if (kNorm) {
-          param8(a.scale, a.mod_bf16, g * a.ld_scale + c, 0.f, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = (1.f + p[i]) * sa[j][i];
-          if (flushed) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += pw[c + i];
-          }
-          store8(pw + c, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = (1.f + p[i]) * ss[j][i];
-          if (flushed) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += pw[a.C + c + i];
-          }
-          store8(pw + a.C + c, v);
-        }
-        if (kBranch) {
-          param8(a.gate, a.mod_bf16, g * a.ld_gate + c, 1.f, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = p[i] * sd[j][i];
-          if (flushed) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += pw[2 * a.C + c + i];
-          }
-          store8(pw + 2 * a.C + c, v);
-        }
-      }
-      if (whole) {
-        if (kNorm && a.dscale) {
-          param8(a.w, a.w_bf16, c, 1.f, p);
-          param8(a.b, a.w_bf16, c, 0.f, q);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = fmaf(p[i], sa[j][i], q[i] * ss[j][i]);
-          store_param8(a.dscale, a.mod_bf16, g * a.C + c, v);
-        }
-        if (kNorm && a.dshift) store_param8(a.dshift, a.mod_bf16, g * a.C + c, ss[j]);
-        if (kBranch && a.dgate) {
-          param8(a.pw, a.w_bf16, c, 1.f, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = p[i] * sd[j][i];
-          store_param8(a.dgate, a.mod_bf16, g * a.C + c, v);
-        }
-      } else if (a.part_g) {
-        if (kNorm) {
-          store8(pg + c, sa[j]);
-          store8(pg + a.C + c, ss[j]);
-        }
-        if (kBranch) store8(pg + 2 * a.C + c, sd[j]);
-      }
-    }
-    flushed = true;
-  };
   int buf = 0, at_stage = 0;
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f), st_next = st;
   if (a.st) st_next = __ldg(a.st + r0);
-  for (long long r = r0; r < r1; ++r) {
-    fetch(r + a.depth - 1);
-    st = st_next;
-    if (a.st && r + 1 < r1) st_next = __ldg(a.st + r + 1);
-    if (r >= g_end) {
-      if (r > r0) flush(r);
+  for (int r = r0;; ++r) {
+    if (r >= g_end || r == r1) {
+      if (r > r0) {
+        flush<kV, kBranch, kNorm>(a, sum, g, g * a.group >= r0 && (g + 1) * a.group <= r,
+                                  g == g_first, flushed);
+        flushed = true;
+      }
+      if (r == r1) break;
       g = r / a.group;
       g_end = (g + 1) * a.group;
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        const long long c = ok[j] ? col[j] : 0;
-        float p[8];
+        const long long c = ok[j] ? tid * 8 + j * next : 0;
+        f2 p[4];
         if (kBranch) {
           param8(a.gate, a.mod_bf16, g * a.ld_gate + c, 1.f, G[j]);
           param8(a.pw, a.w_bf16, c, 1.f, p);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) G[j][i] *= p[i];
+          for (int i = 0; i < 4; ++i) G[j][i] = mul2(G[j][i], p[i]);
         }
         if (kNorm) {
           param8(a.scale, a.mod_bf16, g * a.ld_scale + c, 0.f, p);
           param8(a.w, a.w_bf16, c, 1.f, S[j]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) S[j][i] *= 1.f + p[i];
+          for (int i = 0; i < 4; ++i) S[j][i] = mul2(S[j][i], add2(p[i], both(1.f)));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sa[j][i] = ss[j][i] = sd[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) sum.a[j][i] = sum.s[j][i] = sum.d[j][i] = 0;
       }
     }
-    copy_wait(a.depth);
-    const char* at = ring + at_stage * stage;
-    at_stage = at_stage + 1 == a.depth ? 0 : at_stage + 1;
-    float t[kV][8];
+    fetch();
+    st = st_next;
+    if (a.st && r + 1 < r1) st_next = __ldg(a.st + r + 1);
+    ring_wait(a.depth);
+    const char* at = ring + at_stage;
+    at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
+    f2 t[kV][4];
     if (kNorm) {
-      float xh[kV][8], s1 = 0.f, s2 = 0.f;
+      const f2 m = both(-st.x), s = both(st.y);
+      f2 xh[kV][4], s1 = 0, s2 = 0;
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
-          Slot<TX>::take(at + o_x, j, threads, xh[j]);
-          Slot<TY>::take(at + o_gh, j, threads, t[j]);
+          take<TX>(at + o_x, j, xh[j]);
+          take<TY>(at + o_gh, j, t[j]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xh[j][i] = (xh[j][i] - st.x) * st.y;
-            sa[j][i] = fmaf(t[j][i], xh[j][i], sa[j][i]);
-            ss[j][i] += t[j][i];
-            t[j][i] *= S[j][i];
-            s1 += t[j][i];
-            s2 = fmaf(t[j][i], xh[j][i], s2);
+          for (int i = 0; i < 4; ++i) {
+            xh[j][i] = mul2(add2(xh[j][i], m), s);
+            sum.a[j][i] = fma2(t[j][i], xh[j][i], sum.a[j][i]);
+            sum.s[j][i] = add2(sum.s[j][i], t[j][i]);
+            t[j][i] = mul2(t[j][i], S[j][i]);
+            s1 = add2(s1, t[j][i]);
+            s2 = fma2(t[j][i], xh[j][i], s2);
           }
         }
-      const float2 s = row_sum2(s1, s2, sm, buf);
-      const float c1 = a.norm == BASA_NORM_LAYER ? s.x * a.inv : 0.f, c2 = s.y * a.inv;
+      const float2 v = row_sum2(s1, s2, sm, buf);
+      // t = rstd (a - mean(a) - xh mean(a xh)) + gx
+      const f2 c1 = both(a.norm == BASA_NORM_LAYER ? -v.x * a.inv : 0.f), c2 = both(-v.y * a.inv);
 #pragma unroll
       for (int j = 0; j < kV; ++j)
         if (ok[j]) {
-          float gx[8];
+          f2 gx[4] = {0, 0, 0, 0};
+          if (a.gx) take<TX>(at, j, gx);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) gx[i] = 0.f;
-          if (a.gx) Slot<TX>::take(at + o_gx, j, threads, gx);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[j][i] = fmaf(st.y, t[j][i] - c1 - xh[j][i] * c2, gx[i]);
+          for (int i = 0; i < 4; ++i)
+            t[j][i] = fma2(s, add2(fma2(xh[j][i], c2, t[j][i]), c1), gx[i]);
         }
     } else {
 #pragma unroll
       for (int j = 0; j < kV; ++j)
-        if (ok[j]) Slot<TX>::take(at + o_gx, j, threads, t[j]);
+        if (ok[j]) take<TX>(at, j, t[j]);
     }
+    const f2 res = both(a.res);
 #pragma unroll
     for (int j = 0; j < kV; ++j)
       if (ok[j]) {
-        float v[8];
+        f2 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = a.res * t[j][i];
-        store8(static_cast<TX*>(a.dx) + r * a.C + col[j], v);
+        for (int i = 0; i < 4; ++i) v[i] = mul2(res, t[j][i]);
+        store8(static_cast<TX*>(a.dx) + to + j * next, v);
       }
     if (kBranch) {
-      const bool norm_y = a.post != BASA_NORM_NONE;
-      const float pm = norm_y ? st.z : 0.f, ps = norm_y ? st.w : 1.f;
-      float yh[kV][8], s1 = 0.f, s2 = 0.f;
+      if (a.post == BASA_NORM_NONE) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
+        for (int j = 0; j < kV; ++j)
+          if (ok[j]) {
+            if (a.need_y) {
+              f2 y[4];
+              take<TY>(at + o_y, j, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) yh[j][i] = 0.f;
-          if (a.need_y) Slot<TY>::take(at + o_y, j, threads, yh[j]);
+              for (int i = 0; i < 4; ++i) sum.d[j][i] = fma2(t[j][i], y[i], sum.d[j][i]);
+            }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            yh[j][i] = (yh[j][i] - pm) * ps;
-            sd[j][i] = fmaf(t[j][i], yh[j][i], sd[j][i]);
-            t[j][i] *= G[j][i];
-            s1 += t[j][i];
-            s2 = fmaf(t[j][i], yh[j][i], s2);
+            for (int i = 0; i < 4; ++i) t[j][i] = mul2(t[j][i], G[j][i]);
           }
-        }
-      if (norm_y) {
-        const float2 s = row_sum2(s1, s2, sm, buf);
-        const float c1 = a.post == BASA_NORM_LAYER ? s.x * a.inv : 0.f, c2 = s.y * a.inv;
+      } else {
+        const f2 m = both(-st.z), s = both(st.w);
+        f2 yh[kV][4], s1 = 0, s2 = 0;
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+          if (ok[j]) {
+            take<TY>(at + o_y, j, yh[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              yh[j][i] = mul2(add2(yh[j][i], m), s);
+              sum.d[j][i] = fma2(t[j][i], yh[j][i], sum.d[j][i]);
+              t[j][i] = mul2(t[j][i], G[j][i]);
+              s1 = add2(s1, t[j][i]);
+              s2 = fma2(t[j][i], yh[j][i], s2);
+            }
+          }
+        const float2 v = row_sum2(s1, s2, sm, buf);
+        const f2 c1 = both(a.post == BASA_NORM_LAYER ? -v.x * a.inv : 0.f), c2 = both(-v.y * a.inv);
 #pragma unroll
         for (int j = 0; j < kV; ++j)
           if (ok[j])
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[j][i] = ps * (t[j][i] - c1 - yh[j][i] * c2);
+            for (int i = 0; i < 4; ++i)
+              t[j][i] = mul2(s, add2(fma2(yh[j][i], c2, t[j][i]), c1));
       }
 #pragma unroll
       for (int j = 0; j < kV; ++j)
-        if (ok[j]) store8(static_cast<TY*>(a.dy) + r * a.C + col[j], t[j]);
+        if (ok[j]) store8(static_cast<TY*>(a.dy) + to + j * next, t[j]);
     }
+    to += a.C;
   }
-  flush(r1);
 }
 
 // Joins the partial sums of gnorm_bwd_kernel.  A CTA owns eight columns and
@@ -595,18 +603,6 @@ __global__ void __launch_bounds__(256) gnorm_join_kernel(GnJoin a) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return 148;
-  }
-  return n;
-}
-
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 int round32(int x) { return (x + 31) / 32 * 32; }
 
 basa_status check_gnorm(const basa_gnorm_params* p) {
@@ -624,7 +620,7 @@ basa_status check_gnorm(const basa_gnorm_params* p) {
       return ty[i] == BASA_FP8_E4M3 ? BASA_ERR_UNSUPPORTED : BASA_ERR_INVALID_ARG;
   if (p->x_dtype == BASA_BF16 && p->dtype == BASA_F32) return BASA_ERR_UNSUPPORTED;
   if (p->rows % p->groups) return BASA_ERR_SHAPE;
-  if (p->C % 8 || p->C > kMaxC || p->rows > (1LL << 31) || p->groups > (1LL << 31))
+  if (p->C % 8 || p->C > kMaxC || p->rows > (1LL << 30) || p->groups > (1LL << 30))
     return BASA_ERR_UNSUPPORTED;
   const int64_t ld[3] = {p->ld_gate, p->ld_scale, p->ld_shift};
   for (int i = 0; i < 3; ++i) {
@@ -664,14 +660,14 @@ basa_status go(K kernel, const GnArgs& a, unsigned grid, int threads, int smem, 
 template <typename TX, typename TY, int kThreads, int kCtas>
 basa_status go_fwd_t(GnArgs a, int threads, cudaStream_t st) {
   const bool branch = a.y != nullptr, norm = a.norm != BASA_NORM_NONE;
-  const int stage = slot_bytes<TX>(2, threads) + (branch ? slot_bytes<TY>(2, threads) : 0);
+  const int stage = Slot<TX>::bytes(2, threads) + (branch ? Slot<TY>::bytes(2, threads) : 0);
   a.depth = 3;
   const int smem = a.depth * stage;
   int per_sm = kSmemCta / (smem + 1024);
   const int by_regs = kThreads * kCtas / threads;
   if (per_sm > by_regs) per_sm = by_regs;
   if (per_sm < 1) per_sm = 1;
-  const long long cap = (long long)sm_count() * per_sm;
+  const long long cap = (long long)row_sm_count() * per_sm;
   const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
   if (branch && norm)
     return go(gnorm_kernel<TX, TY, 2, kThreads, kCtas, true, true>, a, grid, threads, smem, st);
@@ -701,7 +697,7 @@ BwdShape bwd_shape(const basa_gnorm_params* p) {
   s.threads = round32((nvec + s.v - 1) / s.v);
   int per_sm = (s.v == 1 ? 640 : 512) / s.threads;
   if (per_sm > 8) per_sm = 8;
-  long long cap = (long long)sm_count() * per_sm;
+  long long cap = (long long)row_sm_count() * per_sm;
   const long long few = (p->rows + 3) / 4;  // at least four rows a CTA
   if (cap > few) cap = few;
   s.grid = cap < 1 ? 1 : cap;
@@ -717,7 +713,7 @@ size_t part_w_bytes(const basa_gnorm_params* p, const BwdShape& s) {
 template <typename TX, typename TY, int kV, int kThreads>
 basa_status go_bwd_v(GnArgs a, const BwdShape& s, cudaStream_t st) {
   const bool branch = a.dy != nullptr, norm = a.norm != BASA_NORM_NONE;
-  const int xb = slot_bytes<TX>(kV, s.threads), yb = slot_bytes<TY>(kV, s.threads);
+  const int xb = Slot<TX>::bytes(kV, s.threads), yb = Slot<TY>::bytes(kV, s.threads);
   const int stage = (a.gx ? xb : 0) + (a.need_y ? yb : 0) + (norm ? xb + yb : 0);
   const int ctas = (kV == 1 ? 640 : 512) / s.threads;
   const int room = kSmemCta / (ctas < 1 ? 1 : ctas > 8 ? 8 : ctas) - 1024;

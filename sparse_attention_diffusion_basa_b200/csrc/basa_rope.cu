@@ -26,7 +26,7 @@ struct RopePart {      // one of q, k, v
   long long ldx, ldg, ldo;
   int heads;
   int chunks;          // CTAs that share a token's heads
-  int steps;           // of kHeadsPerWarp heads, per chunk
+  int steps;           // of 512 / d heads each, per chunk
   float mul;           // e4m3 output: 1 / descale
 };
 
@@ -44,248 +44,491 @@ __device__ __forceinline__ RopePart pick(const RopeArgs& a, int part) {
   return part == 0 ? a.q : part == 1 ? a.k : a.v;
 }
 
-// The rotation of the eight elements at 8 * sub of a head: element i and its
-// partner share cs[pair(i)].  Pairs of neighbours: four angles.  Pairs half the
-// rotated width apart: eight, the partner's elements lie in another lane.
+// A lane holds sixteen elements of a head: two vectors of eight, at ea and eb.
+// They are kept as eight packed pairs A[4], B[4] such that (A[i], B[i]) are the
+// first and second elements of rotated pairs, whatever the layout, so that the
+// rotation is A' = A cos - B sin, B' = B cos + A sin without a word exchanged
+// between lanes:
+//   pairs    A the even and B the odd elements of both vectors,
+//   halves   A the vector in the first and B the one in the second half of the
+//            rotated width (of the rest, two vectors that are not rotated).
+struct Lane {
+  int ea, eb;   // elements
+  int ja, jb;   // rotated pair of A[0] and of A[2]; -1: not rotated
+};
 template <bool kHalves>
-struct Turn {
-  static constexpr int kN = kHalves ? 8 : 4;
-  int base[kN];
-  uint32_t axis;   // two bits a pair; 3: not rotated
-  float sign;      // halves: -1 for the first element of a pair, +1 for the second
-  int partner;     // halves: lane that holds the partner's elements
-  float2 cs[kN];
-
-  __device__ __forceinline__ void init(const RopeArgs& a, int sub, int lanes_per_head) {
-    const int pairs = a.nt + a.nh + a.nw;
-    const int lane = threadIdx.x & 31;
-    int j0 = sub * 4;
-    sign = 1.f;
-    partner = lane;
-    if (kHalves) {
-      j0 = sub * 8;
-      if (j0 < pairs) {
-        sign = -1.f;
-        partner = lane + pairs / 8;
-      } else if (j0 < 2 * pairs) {
-        j0 -= pairs;
-        partner = lane - pairs / 8;
-      } else {
-        j0 = pairs;
-      }
-    }
-    axis = 0;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int j = j0 + i;
-      uint32_t ax = 3;
-      base[i] = 0;
-      if (j < a.nt) {
-        ax = 0;
-        base[i] = j;
-      } else if (j < a.nt + a.nh) {
-        ax = 1;
-        base[i] = (int)a.T * a.nt + j - a.nt;
-      } else if (j < pairs) {
-        ax = 2;
-        base[i] = (int)a.T * a.nt + (int)a.Hg * a.nh + j - a.nt - a.nh;
-      }
-      axis |= ax << (2 * i);
-    }
-  }
-
-  // The angles of token n; dir = -1 turns back.
-  __device__ __forceinline__ void load(const RopeArgs& a, uint32_t n, float dir) {
-    const uint32_t row = n / a.Wg, x = n - row * a.Wg;
-    const uint32_t frame = row / a.Hg, y = row - frame * a.Hg;
-    const uint32_t t = frame % a.T;
-    const int ot = (int)t * a.nt, oy = (int)y * a.nh, ox = (int)x * a.nw;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const uint32_t ax = (axis >> (2 * i)) & 3u;
-      float2 v = make_float2(1.f, 0.f);
-      if (ax != 3u) v = __ldg(a.table + base[i] + (ax == 0u ? ot : ax == 1u ? oy : ox));
-      v.y *= kHalves ? dir * sign : dir;
-      cs[i] = v;
-    }
-  }
-
-  __device__ __forceinline__ void apply(float (&f)[8]) const {
-    if (kHalves) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(0xffffffffu, f[i], partner);
-        f[i] = f[i] * cs[i & (kN - 1)].x + other * cs[i & (kN - 1)].y;
-      }
+__device__ __forceinline__ Lane lane_of(const RopeArgs& a, int sub) {
+  const int pairs = a.nt + a.nh + a.nw;
+  Lane l;
+  if (kHalves) {
+    const int r = pairs / 8;  // lanes of the rotated width
+    if (sub < r) {
+      l.ea = 8 * sub;
+      l.eb = l.ea + pairs;
+      l.ja = 8 * sub;
+      l.jb = l.ja + 4;
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = f[2 * i], q = f[2 * i + 1];
-        f[2 * i] = p * cs[i].x - q * cs[i].y;
-        f[2 * i + 1] = p * cs[i].y + q * cs[i].x;
-      }
+      l.ea = 2 * pairs + 8 * (sub - r);
+      l.eb = l.ea + (a.d - 2 * pairs) / 2;
+      l.ja = l.jb = -1;
     }
+  } else {
+    l.ea = 8 * sub;
+    l.eb = l.ea + a.d / 2;
+    l.ja = l.ea / 2;
+    l.jb = l.eb / 2;
+  }
+  return l;
+}
+
+template <bool kHalves, typename T>
+__device__ __forceinline__ void unpack16(const Raw8<T>& a, const Raw8<T>& b, f2 (&A)[4],
+                                         f2 (&B)[4]) {
+  if (kHalves) {
+    widen8(a, A);
+    widen8(b, B);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      A[i] = pk(elem(a, 4 * i), elem(a, 4 * i + 2));
+      B[i] = pk(elem(a, 4 * i + 1), elem(a, 4 * i + 3));
+      A[i + 2] = pk(elem(b, 4 * i), elem(b, 4 * i + 2));
+      B[i + 2] = pk(elem(b, 4 * i + 1), elem(b, 4 * i + 3));
+    }
+  }
+}
+template <bool kHalves>
+__device__ __forceinline__ void order16(const f2 (&A)[4], const f2 (&B)[4], float (&a)[8],
+                                        float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = un(A[i]), q = un(B[i]);
+    if (kHalves) {
+      a[2 * i] = p.x;
+      a[2 * i + 1] = p.y;
+      b[2 * i] = q.x;
+      b[2 * i + 1] = q.y;
+    } else {
+      float* f = i < 2 ? a + 4 * i : b + 4 * (i - 2);
+      f[0] = p.x;
+      f[1] = q.x;
+      f[2] = p.y;
+      f[3] = q.y;
+    }
+  }
+}
+template <bool kHalves, typename TO>
+__device__ __forceinline__ void pack16(TO* row, const Lane& l, const f2 (&A)[4], const f2 (&B)[4]) {
+  float a[8], b[8];
+  order16<kHalves>(A, B, a, b);
+  store8(row + l.ea, a);
+  store8(row + l.eb, b);
+}
+// A lane's sixteen weights from element `col` of w on, in the order of A and B.
+template <bool kHalves>
+__device__ __forceinline__ void weight16(const void* w, bool bf16, int col, const Lane& l,
+                                         f2 (&A)[4], f2 (&B)[4]) {
+  Raw8<float> a, b;
+  float fa[8], fb[8];
+  param8(w, bf16, col + l.ea, 1.f, fa);
+  param8(w, bf16, col + l.eb, 1.f, fb);
+  a.a = make_uint4(__float_as_uint(fa[0]), __float_as_uint(fa[1]), __float_as_uint(fa[2]),
+                   __float_as_uint(fa[3]));
+  a.b = make_uint4(__float_as_uint(fa[4]), __float_as_uint(fa[5]), __float_as_uint(fa[6]),
+                   __float_as_uint(fa[7]));
+  b.a = make_uint4(__float_as_uint(fb[0]), __float_as_uint(fb[1]), __float_as_uint(fb[2]),
+                   __float_as_uint(fb[3]));
+  b.b = make_uint4(__float_as_uint(fb[4]), __float_as_uint(fb[5]), __float_as_uint(fb[6]),
+                   __float_as_uint(fb[7]));
+  unpack16<kHalves>(a, b, A, B);
+}
+
+// Where pair j's angle lies in the table: base + coordinate of its axis * pairs
+// of the axis.
+struct Spot {
+  int base, axis;  // axis 3: not rotated
+};
+__device__ __forceinline__ Spot spot_of(const RopeArgs& a, int j) {
+  const int pairs = a.nt + a.nh + a.nw;
+  if (j < 0 || j >= pairs) return {0, 3};
+  if (j < a.nt) return {j, 0};
+  if (j < a.nt + a.nh) return {(int)a.T * a.nt + j - a.nt, 1};
+  return {(int)a.T * a.nt + (int)a.Hg * a.nh + j - a.nt - a.nh, 2};
+}
+
+// Grid coordinates of a token, stepped by a fixed number of tokens without a
+// division.
+struct Coord {
+  uint32_t x, y, t, sx, sy, st;
+  __device__ __forceinline__ void init(const RopeArgs& a, uint32_t n, uint32_t step) {
+    uint32_t q = n / a.Wg;
+    x = n - q * a.Wg;
+    t = q / a.Hg;
+    y = q - t * a.Hg;
+    t %= a.T;
+    q = step / a.Wg;
+    sx = step - q * a.Wg;
+    st = q / a.Hg;
+    sy = q - st * a.Hg;
+    st %= a.T;
+  }
+  __device__ __forceinline__ void next(const RopeArgs& a) {
+    x += sx;
+    y += sy;
+    t += st;
+    if (x >= a.Wg) {
+      x -= a.Wg;
+      ++y;
+    }
+    if (y >= a.Hg) {
+      y -= a.Hg;
+      ++t;
+    }
+    if (t >= a.T) t -= a.T;
+  }
+  __device__ __forceinline__ float2 angle(const RopeArgs& a, const Spot& s) const {
+    const int off = s.axis == 0 ? (int)t * a.nt : s.axis == 1 ? (int)y * a.nh : (int)x * a.nw;
+    return s.axis == 3 ? make_float2(1.f, 0.f) : __ldg(a.table + s.base + off);
   }
 };
 
-constexpr int kRopeThreads = 256;
+__device__ __forceinline__ f2 neg2(f2 v) {
+  const float2 f = un(v);
+  return pk(-f.x, -f.y);
+}
+
+constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeBatch = 4;  // steps whose loads are issued together
+
+// Which of q, k, v a CTA works on, and the chunk of its heads.
+__device__ __forceinline__ int part_of(const RopeArgs& a, int& chunk) {
+  chunk = blockIdx.y;
+  if (chunk < a.q.chunks) return 0;
+  chunk -= a.q.chunks;
+  if (chunk < a.k.chunks) return 1;
+  chunk -= a.k.chunks;
+  return 2;
+}
+
+// v: rows copied (or narrowed) two heads' worth at a time.
+template <typename TI, typename TO, int kLph, bool kHalves>
+__device__ __forceinline__ void copy_rows(const TI* x, TO* o, const Lane& l, int h0, int hend,
+                                          float mul) {
+  constexpr int kHpw = 32 / kLph, kD = kLph * 16;
+  for (int h = h0; h < hend; h += 2 * kHpw) {
+    Raw8<TI> ra[2], rb[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (h + u * kHpw < hend) {
+        load8(ra[u], x + (h + u * kHpw) * kD + l.ea);
+        load8(rb[u], x + (h + u * kHpw) * kD + l.eb);
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (h + u * kHpw < hend) {
+        f2 A[4], B[4];
+        unpack16<kHalves>(ra[u], rb[u], A, B);
+        if (sizeof(TO) == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            A[i] = mul2(A[i], pk(mul, mul));
+            B[i] = mul2(B[i], pk(mul, mul));
+          }
+        }
+        pack16<kHalves>(o + (h + u * kHpw) * kD, l, A, B);
+      }
+  }
+}
+
+// A warp's two pairs a lane of one token's angles, gathered ahead of the token
+// and then read by the lanes that need them.
+struct Gather {
+  Coord at;
+  Spot spot[2];
+  float2 next[2];
+  __device__ __forceinline__ void init(const RopeArgs& a, uint32_t n, uint32_t step, int first,
+                                       int threads) {
+    at.init(a, n, step);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = first + i * threads;
+      spot[i] = spot_of(a, j < 64 ? j : -1);
+      next[i] = at.angle(a, spot[i]);
+    }
+  }
+  __device__ __forceinline__ void put(float4* to, int first, int threads) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (first + i * threads < 64) reinterpret_cast<float2*>(to)[first + i * threads] = next[i];
+  }
+  // Past the last token the coordinates are those of some token all the same.
+  __device__ __forceinline__ void ahead(const RopeArgs& a) {
+    at.next(a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) next[i] = at.angle(a, spot[i]);
+  }
+};
+
+__device__ __forceinline__ void angles_of(const float4* cs, const Lane& l, f2 (&C)[4],
+                                          f2 (&S)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = i < 2 ? l.ja : l.jb;
+    float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (j >= 0) v = cs[j / 2 + (i & 1)];
+    C[i] = pk(v.x, v.z);
+    S[i] = pk(v.y, v.w);
+  }
+}
+
+// Stages of a warp's ring: 4 KB of reads in flight a warp, 2 KB for fp32's half
+// as many values a byte.
+template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
 
 // Norm over each head, or none.  kLph lanes hold a head, a warp 32 / kLph heads
 // (a step); a warp takes the steps of its chunk of one token, then the next
-// token, so that a token's angles are read once for all its heads and a
-// thread's columns of the weight stay in registers.
+// token, so that a token's angles are read once for all its heads.  Rows come
+// through a ring of asynchronous copies, private to each lane, that runs ahead
+// across tokens.  The norm's weight is folded into the angles:
+// A' = r (A (wA cos) - B (wB sin)).
 template <typename TI, typename TO, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) rope_head_kernel(RopeArgs a) {
-  constexpr int kHpw = 32 / kLph;
-  int chunk = blockIdx.y, part = 0;
-  if (chunk >= a.q.chunks) {
-    chunk -= a.q.chunks;
-    part = 1;
-    if (chunk >= a.k.chunks) {
-      chunk -= a.k.chunks;
-      part = 2;
-    }
-  }
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(RopeArgs a) {
+  constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<TI>;
+  constexpr int kStage = Slot<TI>::bytes(2, 32);
+  __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
+  __shared__ float4 cs[kRopeWarps][2][32];
+  int chunk;
+  const int part = part_of(a, chunk);
   const RopePart P = pick(a, part);
-  const int lane = threadIdx.x & 31, sub = lane % kLph, slot = lane / kLph;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, slot = lane / kLph;
   const int h0 = chunk * P.steps * kHpw + slot;
   const int hend = min(P.heads, (chunk + 1) * P.steps * kHpw);
   const uint32_t stride = gridDim.x * kRopeWarps;
-  Turn<kHalves> turn;
-  float w[8];
-  if (part < 2) {
-    turn.init(a, sub, kLph);
-    if (kNorm) param8(P.w, a.w_bf16, sub * 8, 1.f, w);
+  const Lane l = lane_of<kHalves>(a, lane % kLph);
+  uint32_t n = blockIdx.x * kRopeWarps + warp;
+  const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx;
+  TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo;
+  const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
+  if (part == 2) {
+    for (; n < a.tokens; n += stride, x += dx, o += dout)
+      copy_rows<TI, TO, kLph, kHalves>(x, o, l, h0, hend, P.mul);
+    return;
   }
-  for (uint32_t n = blockIdx.x * kRopeWarps + threadIdx.x / 32; n < a.tokens; n += stride) {
-    const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx + sub * 8;
-    TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo + sub * 8;
-    if (part < 2) turn.load(a, n, 1.f);
-    for (int s = 0; s < P.steps; s += kRopeBatch) {
-      Raw8<TI> raw[kRopeBatch];
-#pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int h = h0 + (s + u) * kHpw;
-        if (h < hend)
-          load8(raw[u], x + h * (kLph * 8));
-        else
-          zero8(raw[u]);
+  if (n >= a.tokens) return;  // a whole warp; the kernel has no CTA barrier
+  const uint32_t ring = shared_u32(rings[warp]);
+  uint32_t fn = n;
+  int fh = h0, to = 0;
+  auto fetch = [&]() {
+    if (fn < a.tokens) {
+      if (fh < hend) {
+        Slot<TI>::fetch(ring + to, x + fh * kD + l.ea, 0, 32, lane);
+        Slot<TI>::fetch(ring + to, x + fh * kD + l.eb, 1, 32, lane);
       }
-#pragma unroll
-      for (int u = 0; u < kRopeBatch; ++u) {
-        const int h = h0 + (s + u) * kHpw;
-        float f[8];
-        widen8(raw[u], f);
-        if (part < 2) {
-          if (kNorm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-            const float r = rsqrtf(lane_sum<kLph>(ss) * (1.f / (kLph * 8)) + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
-          }
-          turn.apply(f);
-        }
-        if (sizeof(TO) == 1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= P.mul;
-        }
-        if (h < hend) store8(o + h * (kLph * 8), f);
+      fh += kHpw;
+      if (fh - slot >= hend) {
+        fh = h0;
+        fn += stride;
+        x += dx;
       }
+    }
+    copy_commit();
+    to = to + kStage == kDepth * kStage ? 0 : to + kStage;
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) fetch();
+  Gather ang;
+  ang.init(a, n, stride, lane, 32);
+  f2 WA[4], WB[4];
+  if (kNorm) weight16<kHalves>(P.w, a.w_bf16, 0, l, WA, WB);
+  const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
+  int from = 0, buf = 0;
+  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
+    ang.put(cs[warp][buf], lane, 32);
+    __syncwarp();
+    ang.ahead(a);
+    f2 CA[4], CB[4], SA[4], SB[4];
+    angles_of(cs[warp][buf], l, CA, SA);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      CB[i] = CA[i];
+      SB[i] = neg2(SA[i]);
+      if (kNorm) {
+        CA[i] = mul2(CA[i], WA[i]);
+        CB[i] = mul2(CB[i], WB[i]);
+        SA[i] = mul2(SA[i], WA[i]);
+        SB[i] = mul2(SB[i], WB[i]);
+      }
+    }
+    for (int h = h0; h - slot < hend; h += kHpw) {  // the same trip count for a warp
+      fetch();
+      copy_wait<kDepth - 1>();
+      Raw8<TI> ra, rb;
+      zero8(ra);
+      zero8(rb);
+      if (h < hend) {
+        Slot<TI>::take(rings[warp] + from, 0, 32, lane, ra);
+        Slot<TI>::take(rings[warp] + from, 1, 32, lane, rb);
+      }
+      from = from + kStage == kDepth * kStage ? 0 : from + kStage;
+      f2 A[4], B[4];
+      unpack16<kHalves>(ra, rb, A, B);
+      float r = mul;
+      if (kNorm) {
+        f2 s0 = mul2(A[0], A[0]), s1 = mul2(B[0], B[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          s0 = fma2(A[i], A[i], s0);
+          s1 = fma2(B[i], B[i], s1);
+        }
+        r *= rsqrtf(lane_sum<kLph>(sum2(add2(s0, s1))) * (1.f / kD) + a.eps);
+      }
+      const f2 rr = pk(r, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 p = fma2(A[i], CA[i], mul2(B[i], SB[i]));
+        const f2 q = fma2(B[i], CB[i], mul2(A[i], SA[i]));
+        A[i] = kNorm || sizeof(TO) == 1 ? mul2(p, rr) : p;
+        B[i] = kNorm || sizeof(TO) == 1 ? mul2(q, rr) : q;
+      }
+      if (h < hend) pack16<kHalves>(o + h * kD, l, A, B);
     }
   }
 }
 
-constexpr int kRopeBwdBatch = 2;
-
 // Backward of rope_head_kernel, the same walk.  The weight's gradient is summed
-// in a thread's own eight columns over all its tokens and heads, then over the
+// in a lane's own sixteen columns over all its tokens and heads, then over the
 // CTA, and left as one row of partial sums a CTA.
 template <typename T, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) rope_head_bwd_kernel(RopeArgs a) {
-  constexpr int kHpw = 32 / kLph;
-  constexpr int kD = kLph * 8;
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs a) {
+  constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<T>;
+  constexpr int kStage = Slot<T>::bytes(kNorm ? 4 : 2, 32);
+  __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
+  __shared__ float4 cs[kRopeWarps][2][32];
   __shared__ float red[kRopeWarps][kD];
-  int chunk = blockIdx.y, part = 0;
-  if (chunk >= a.q.chunks) {
-    chunk -= a.q.chunks;
-    part = 1;
-    if (chunk >= a.k.chunks) {
-      chunk -= a.k.chunks;
-      part = 2;
-    }
-  }
+  int chunk;
+  const int part = part_of(a, chunk);
   const RopePart P = pick(a, part);
-  const int lane = threadIdx.x & 31, sub = lane % kLph, slot = lane / kLph;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, slot = lane / kLph;
   const int h0 = chunk * P.steps * kHpw + slot;
   const int hend = min(P.heads, (chunk + 1) * P.steps * kHpw);
   const uint32_t stride = gridDim.x * kRopeWarps;
-  Turn<kHalves> turn;
-  float w[8], acc[8];
-  if (part < 2) {
-    turn.init(a, sub, kLph);
-    if (kNorm) param8(P.w, a.w_bf16, sub * 8, 1.f, w);
+  const Lane l = lane_of<kHalves>(a, lane % kLph);
+  uint32_t n = blockIdx.x * kRopeWarps + warp;
+  const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg;
+  T* o = static_cast<T*>(P.o) + (long long)n * P.ldo;
+  const long long dg = (long long)stride * P.ldg, dout = (long long)stride * P.ldo;
+  if (part == 2) {
+    for (; n < a.tokens; n += stride, g += dg, o += dout)
+      copy_rows<T, T, kLph, kHalves>(g, o, l, h0, hend, 1.f);
+    return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (uint32_t n = blockIdx.x * kRopeWarps + threadIdx.x / 32; n < a.tokens; n += stride) {
-    const T* x = static_cast<const T*>(P.x) + (long long)n * P.ldx + sub * 8;
-    const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg + sub * 8;
-    T* o = static_cast<T*>(P.o) + (long long)n * P.ldo + sub * 8;
-    if (part < 2) turn.load(a, n, -1.f);
-    for (int s = 0; s < P.steps; s += kRopeBwdBatch) {
-      Raw8<T> rg[kRopeBwdBatch], rx[kRopeBwdBatch];
-#pragma unroll
-      for (int u = 0; u < kRopeBwdBatch; ++u) {
-        const int h = h0 + (s + u) * kHpw;
-        zero8(rg[u]);
-        zero8(rx[u]);
-        if (h < hend) {
-          load8(rg[u], g + h * kD);
-          if (kNorm && part < 2) load8(rx[u], x + h * kD);
+  const T* x = kNorm ? static_cast<const T*>(P.x) + (long long)n * P.ldx : nullptr;
+  const long long dx = (long long)stride * P.ldx;
+  const uint32_t ring = shared_u32(rings[warp]);
+  uint32_t fn = n;
+  int fh = h0, to = 0;
+  auto fetch = [&]() {
+    if (fn < a.tokens) {
+      if (fh < hend) {
+        Slot<T>::fetch(ring + to, g + fh * kD + l.ea, 0, 32, lane);
+        Slot<T>::fetch(ring + to, g + fh * kD + l.eb, 1, 32, lane);
+        if (kNorm) {
+          Slot<T>::fetch(ring + to, x + fh * kD + l.ea, 2, 32, lane);
+          Slot<T>::fetch(ring + to, x + fh * kD + l.eb, 3, 32, lane);
         }
       }
-#pragma unroll
-      for (int u = 0; u < kRopeBwdBatch; ++u) {
-        const int h = h0 + (s + u) * kHpw;
-        float f[8];
-        widen8(rg[u], f);
-        if (part < 2) {
-          turn.apply(f);
-          if (kNorm) {
-            float xf[8];
-            widen8(rx[u], xf);
-            float ss = 0.f, sd = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ss = fmaf(xf[i], xf[i], ss);
-              sd = fmaf(xf[i], f[i] * w[i], sd);
-            }
-            ss = lane_sum<kLph>(ss);
-            sd = lane_sum<kLph>(sd);
-            const float r = rsqrtf(ss * (1.f / kD) + a.eps);
-            const float c = sd * (1.f / kD) * r * r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[i] = fmaf(f[i], xf[i] * r, acc[i]);
-              f[i] = r * (f[i] * w[i] - xf[i] * c);
-            }
-          }
-        }
-        if (h < hend) store8(o + h * kD, f);
+      fh += kHpw;
+      if (fh - slot >= hend) {
+        fh = h0;
+        fn += stride;
+        g += dg;
+        if (kNorm) x += dx;
       }
     }
+    copy_commit();
+    to = to + kStage == kDepth * kStage ? 0 : to + kStage;
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) fetch();
+  Gather ang;
+  ang.init(a, n, stride, lane, 32);
+  f2 WA[4], WB[4], accA[4], accB[4];
+  if (kNorm) weight16<kHalves>(P.w, a.w_bf16, 0, l, WA, WB);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
+  int from = 0, buf = 0;
+  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
+    ang.put(cs[warp][buf], lane, 32);
+    __syncwarp();
+    ang.ahead(a);
+    f2 C[4], S[4];
+    angles_of(cs[warp][buf], l, C, S);
+    for (int h = h0; h - slot < hend; h += kHpw) {  // the same trip count for a warp
+      const bool on = h < hend;
+      fetch();
+      copy_wait<kDepth - 1>();
+      const char* at = rings[warp] + from;
+      from = from + kStage == kDepth * kStage ? 0 : from + kStage;
+      f2 A[4], B[4], GA[4], GB[4];
+      Raw8<T> ra, rb;
+      zero8(ra);
+      zero8(rb);
+      if (on) {
+        Slot<T>::take(at, 0, 32, lane, ra);
+        Slot<T>::take(at, 1, 32, lane, rb);
+      }
+      unpack16<kHalves>(ra, rb, A, B);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // turned back
+        GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
+        GB[i] = fma2(B[i], C[i], neg2(mul2(A[i], S[i])));
+      }
+      if (kNorm) {
+        if (on) {
+          Slot<T>::take(at, 2, 32, lane, ra);
+          Slot<T>::take(at, 3, 32, lane, rb);
+        }
+        unpack16<kHalves>(ra, rb, A, B);
+        f2 s0 = mul2(A[0], A[0]), s1 = mul2(B[0], B[0]);
+        f2 d0 = mul2(A[0], mul2(GA[0], WA[0])), d1 = mul2(B[0], mul2(GB[0], WB[0]));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          s0 = fma2(A[i], A[i], s0);
+          s1 = fma2(B[i], B[i], s1);
+          d0 = fma2(A[i], mul2(GA[i], WA[i]), d0);
+          d1 = fma2(B[i], mul2(GB[i], WB[i]), d1);
+        }
+        const float2 s =
+            lane_sum<kLph>(make_float2(sum2(add2(s0, s1)), sum2(add2(d0, d1))));
+        const float r = rsqrtf(s.x * (1.f / kD) + a.eps);
+        const float c = -s.y * (1.f / kD) * r * r * r;
+        const f2 rr = pk(r, r), cc = pk(c, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 pA = mul2(GA[i], rr), pB = mul2(GB[i], rr);
+          accA[i] = fma2(pA, A[i], accA[i]);
+          accB[i] = fma2(pB, B[i], accB[i]);
+          GA[i] = fma2(pA, WA[i], mul2(A[i], cc));
+          GB[i] = fma2(pB, WB[i], mul2(B[i], cc));
+        }
+      }
+      if (on) pack16<kHalves>(o + h * kD, l, GA, GB);
+    }
   }
-  if (kNorm && part < 2 && P.part) {  // uniform over the CTA
+  if (kNorm && P.part) {  // uniform over the CTA
+    float fa[8], fb[8];
+    order16<kHalves>(accA, accB, fa, fb);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v = acc[i];
 #pragma unroll
-      for (int m = kLph; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-      if (slot == 0) red[threadIdx.x / 32][sub * 8 + i] = v;
+      for (int m = kLph; m < 32; m <<= 1) {
+        fa[i] += __shfl_xor_sync(0xffffffffu, fa[i], m);
+        fb[i] += __shfl_xor_sync(0xffffffffu, fb[i], m);
+      }
+      if (slot == 0) {
+        red[warp][l.ea + i] = fa[i];
+        red[warp][l.eb + i] = fb[i];
+      }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < kD; c += kRopeThreads) {
@@ -297,77 +540,175 @@ __global__ void __launch_bounds__(kRopeThreads) rope_head_bwd_kernel(RopeArgs a)
   }
 }
 
-constexpr int kTokenMaxThreads = 512;
+// Norm over all heads of a token: a CTA takes a token's q or k, sixteen elements
+// of a head kV times a thread, rows through a ring of asynchronous copies.  A
+// token's angles are gathered by one thread a pair into shared memory and read
+// behind the barrier that the row's sum needs anyway.  The weights' columns of a
+// thread lie in shared memory too (fp32, read by that thread alone): in
+// registers they would halve the CTAs of an SM.
+struct TokenSmem {
+  float2 red[2][32];
+  float4 cs[2][32];  // two pairs' (cos, sin)
+};
 
-// Sum over the CTA of one or two values a thread; `buf` alternates between
-// calls, so one barrier a call is enough.
-__device__ __forceinline__ float2 block_sum(float a, float b, float2 (*red)[16], int buf) {
-  a = lane_sum<32>(a);
-  b = lane_sum<32>(b);
-  if ((threadIdx.x & 31) == 0) red[buf][threadIdx.x >> 5] = make_float2(a, b);
+__device__ __forceinline__ float2 block_sum(float2 v, TokenSmem& sm, int buf) {
+  v = lane_sum<32>(v);
+  if ((threadIdx.x & 31) == 0) sm.red[buf][threadIdx.x >> 5] = v;
   __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
-    s.x += red[buf][i].x;
-    s.y += red[buf][i].y;
-  }
-  return s;
+  const int i = threadIdx.x & 31;
+  v = i < (int)(blockDim.x >> 5) ? sm.red[buf][i] : make_float2(0.f, 0.f);
+  return lane_sum<32>(v);
+}
+__device__ __forceinline__ float block_sum(float v, TokenSmem& sm, int buf) {
+  v = lane_sum<32>(v);
+  if ((threadIdx.x & 31) == 0) sm.red[buf][threadIdx.x >> 5].x = v;
+  __syncthreads();
+  const int i = threadIdx.x & 31;
+  return lane_sum<32>(i < (int)(blockDim.x >> 5) ? sm.red[buf][i].x : 0.f);
 }
 
-// Norm over all heads of a token: a CTA holds one token's q, k or v in
-// registers (kV vectors of eight a thread), so its rows are read once.
+// A thread's weights in shared memory: eight 16-byte pieces for each of its kV
+// groups of sixteen, the threads side by side.
+__device__ __forceinline__ void put_weights(char* at, int j, const f2 (&A)[4], const f2 (&B)[4]) {
+  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + (size_t)j * 4 * blockDim.x + threadIdx.x;
+  w[0] = make_ulonglong2(A[0], A[1]);
+  w[blockDim.x] = make_ulonglong2(A[2], A[3]);
+  w[2 * blockDim.x] = make_ulonglong2(B[0], B[1]);
+  w[3 * blockDim.x] = make_ulonglong2(B[2], B[3]);
+}
+__device__ __forceinline__ void get_weights(const char* at, int j, f2 (&A)[4], f2 (&B)[4]) {
+  const ulonglong2* w =
+      reinterpret_cast<const ulonglong2*>(at) + (size_t)j * 4 * blockDim.x + threadIdx.x;
+  ulonglong2 v = w[0];
+  A[0] = v.x;
+  A[1] = v.y;
+  v = w[blockDim.x];
+  A[2] = v.x;
+  A[3] = v.y;
+  v = w[2 * blockDim.x];
+  B[0] = v.x;
+  B[1] = v.y;
+  v = w[3 * blockDim.x];
+  B[2] = v.x;
+  B[3] = v.y;
+}
+__host__ __device__ constexpr int weight_bytes(int kv, int threads) { return kv * threads * 64; }
+
 template <typename TI, typename TO, int kV, bool kHalves>
-__global__ void __launch_bounds__(kTokenMaxThreads) rope_token_kernel(RopeArgs a) {
-  __shared__ float2 red[2][16];
+__global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ TokenSmem sm;
+  constexpr int kDepth = kStages<TI>;
   const int part = blockIdx.y;
   const RopePart P = pick(a, part);
-  const int lph = a.d / 8, nvec = P.heads * lph, tid = threadIdx.x;
+  const int lph = a.d / 16, units = P.heads * lph, tid = threadIdx.x, threads = blockDim.x;
   const float inv = 1.f / (float)(P.heads * a.d);
-  Turn<kHalves> turn;
-  if (part < 2) turn.init(a, tid % lph, lph);
-  int buf = 0;
-  for (uint32_t n = blockIdx.x; n < a.tokens; n += gridDim.x, buf ^= 1) {
-    const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx;
-    TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo;
-    Raw8<TI> raw[kV];
+  const Lane l = lane_of<kHalves>(a, tid % lph);
+  const int h0 = tid / lph * a.d, dh = threads / lph * a.d;  // a thread's heads, in elements
+  const uint32_t stride = gridDim.x;
+  uint32_t n = blockIdx.x, fn = n;
+  const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx + h0;
+  TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo + h0;
+  const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
+  bool on[kV];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      if (i < nvec)
-        load8(raw[j], x + i * 8);
-      else
-        zero8(raw[j]);
+  for (int j = 0; j < kV; ++j) on[j] = j * threads + tid < units;
+  char* weights = dyn;
+  char* ring = dyn + weight_bytes(kV, threads);
+  const int stage = Slot<TI>::bytes(2 * kV, threads);
+  const uint32_t ring_at = shared_u32(ring);
+  int to = 0, from = 0;
+  auto fetch = [&]() {
+    if (fn < a.tokens) {
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (on[j]) {
+          Slot<TI>::fetch(ring_at + to, x + j * dh + l.ea, 2 * j, threads, tid);
+          Slot<TI>::fetch(ring_at + to, x + j * dh + l.eb, 2 * j + 1, threads, tid);
+        }
+      fn += stride;
+      x += dx;
     }
-    float r = 1.f;
-    if (part < 2) {
-      turn.load(a, n, 1.f);
-      float ss = 0.f;
+    copy_commit();
+    to = to + stage == kDepth * stage ? 0 : to + stage;
+  };
+  auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
+    Raw8<TI> ra, rb;
+    zero8(ra);
+    zero8(rb);
+    if (on[j]) {
+      Slot<TI>::take(ring + from, 2 * j, threads, tid, ra);
+      Slot<TI>::take(ring + from, 2 * j + 1, threads, tid, rb);
+    }
+    unpack16<kHalves>(ra, rb, A, B);
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) fetch();
+  const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
+  if (part == 2) {
+    const f2 mm = pk(mul, mul);
+    for (; n < a.tokens; n += stride, o += dout) {
+      fetch();
+      copy_wait<kDepth - 1>();
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        float f[8];
-        widen8(raw[j], f);
+        f2 A[4], B[4];
+        take(j, A, B);
+        if (sizeof(TO) == 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+          for (int i = 0; i < 4; ++i) {
+            A[i] = mul2(A[i], mm);
+            B[i] = mul2(B[i], mm);
+          }
+        }
+        if (on[j]) pack16<kHalves>(o + j * dh, l, A, B);
       }
-      r = rsqrtf(block_sum(ss, 0.f, red, buf).x * inv + a.eps);
+      from = from + stage == kDepth * stage ? 0 : from + stage;
+    }
+    return;
+  }
+  Gather ang;
+  ang.init(a, n, stride, tid, threads);
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    f2 A[4], B[4];
+    weight16<kHalves>(on[j] ? P.w : nullptr, a.w_bf16, h0 + j * dh, l, A, B);
+    put_weights(weights, j, A, B);
+  }
+  int buf = 0;
+  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
+    ang.put(sm.cs[buf], tid, threads);
+    ang.ahead(a);
+    fetch();
+    copy_wait<kDepth - 1>();
+    f2 A[kV][4], B[kV][4], s = pk(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      take(j, A[j], B[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fma2(B[j][i], B[j][i], fma2(A[j][i], A[j][i], s));
+    }
+    from = from + stage == kDepth * stage ? 0 : from + stage;
+    const float r = mul * rsqrtf(block_sum(sum2(s), sm, buf) * inv + a.eps);
+    const f2 rr = pk(r, r);
+    f2 C[4], S[4];
+    angles_of(sm.cs[buf], l, C, S);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      C[i] = mul2(C[i], rr);
+      S[i] = mul2(S[i], rr);
     }
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      float f[8];
-      widen8(raw[j], f);
-      if (part < 2) {
-        float w[8];
-        param8(i < nvec ? P.w : nullptr, a.w_bf16, i * 8, 1.f, w);
+      f2 WA[4], WB[4];
+      get_weights(weights, j, WA, WB);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= r * w[e];
-        turn.apply(f);
+      for (int i = 0; i < 4; ++i) {
+        const f2 p = mul2(A[j][i], WA[i]), q = mul2(B[j][i], WB[i]);
+        A[j][i] = fma2(p, C[i], neg2(mul2(q, S[i])));
+        B[j][i] = fma2(q, C[i], mul2(p, S[i]));
       }
-      if (sizeof(TO) == 1) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= P.mul;
-      }
-      if (i < nvec) store8(o + i * 8, f);
+      if (on[j]) pack16<kHalves>(o + j * dh, l, A[j], B[j]);
     }
   }
 }
@@ -375,85 +716,127 @@ __global__ void __launch_bounds__(kTokenMaxThreads) rope_token_kernel(RopeArgs a
 // Backward of rope_token_kernel.  Both sums of a row (x^2 and w gn x) share one
 // barrier; a thread's columns of the weight's gradient stay in registers over
 // all its tokens and are left as one row of partial sums a CTA.
-template <typename T, int kV, bool kHalves>
-__global__ void __launch_bounds__(kTokenMaxThreads) rope_token_bwd_kernel(RopeArgs a) {
-  __shared__ float2 red[2][16];
+template <typename T, int kThreads, int kCtas, bool kHalves>
+__global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArgs a, int depth) {
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ TokenSmem sm;
   const int part = blockIdx.y;
   const RopePart P = pick(a, part);
-  const int lph = a.d / 8, nvec = P.heads * lph, tid = threadIdx.x;
+  const int lph = a.d / 16, tid = threadIdx.x, threads = blockDim.x;
   const float inv = 1.f / (float)(P.heads * a.d);
-  Turn<kHalves> turn;
-  if (part < 2) turn.init(a, tid % lph, lph);
-  float acc[kV][8];
+  const Lane l = lane_of<kHalves>(a, tid % lph);
+  const int h0 = tid / lph * a.d;
+  const bool on = tid < P.heads * lph;
+  const uint32_t stride = gridDim.x;
+  uint32_t n = blockIdx.x, fn = n;
+  const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg + h0;
+  const T* x = static_cast<const T*>(P.x) + (part < 2 ? (long long)n * P.ldx + h0 : 0);
+  T* o = static_cast<T*>(P.o) + (long long)n * P.ldo + h0;
+  const long long dg = (long long)stride * P.ldg, dout = (long long)stride * P.ldo,
+                  dx = part < 2 ? (long long)stride * P.ldx : 0;
+  char* weights = dyn;
+  char* ring = dyn + weight_bytes(1, threads);
+  const int stage = Slot<T>::bytes(4, threads);
+  const uint32_t ring_at = shared_u32(ring);
+  int to = 0, from = 0;
+  auto fetch = [&]() {
+    if (fn < a.tokens && on) {
+      Slot<T>::fetch(ring_at + to, g + l.ea, 0, threads, tid);
+      Slot<T>::fetch(ring_at + to, g + l.eb, 1, threads, tid);
+      if (part < 2) {
+        Slot<T>::fetch(ring_at + to, x + l.ea, 2, threads, tid);
+        Slot<T>::fetch(ring_at + to, x + l.eb, 3, threads, tid);
+      }
+    }
+    fn += stride;  // at most twice the CTAs past the tokens, far from 2^32
+    g += dg;
+    x += dx;
+    copy_commit();
+    to = depth == 2 ? stage - to : 0;
+  };
+  auto arrive = [&]() {  // the oldest row asked for
+    if (depth == 2)
+      copy_wait<1>();
+    else
+      copy_wait<0>();
+  };
+  auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
+    Raw8<T> ra, rb;
+    zero8(ra);
+    zero8(rb);
+    if (on) {
+      Slot<T>::take(ring + from, j, threads, tid, ra);
+      Slot<T>::take(ring + from, j + 1, threads, tid, rb);
+    }
+    unpack16<kHalves>(ra, rb, A, B);
+  };
+  if (depth == 2) fetch();
+  if (part == 2) {
+    for (; n < a.tokens; n += stride, o += dout) {
+      fetch();
+      arrive();
+      f2 A[4], B[4];
+      take(0, A, B);
+      from = depth == 2 ? stage - from : 0;
+      if (on) pack16<kHalves>(o, l, A, B);
+    }
+    return;
+  }
+  Gather ang;
+  ang.init(a, n, stride, tid, threads);
+  ang.put(sm.cs[0], tid, threads);
+  f2 accA[4], accB[4];
+  {
+    f2 A[4], B[4];
+    weight16<kHalves>(on ? P.w : nullptr, a.w_bf16, h0, l, A, B);
+    put_weights(weights, 0, A, B);
 #pragma unroll
-  for (int j = 0; j < kV; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[j][e] = 0.f;
+    for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
+  }
+  __syncthreads();
   int buf = 0;
-  for (uint32_t n = blockIdx.x; n < a.tokens; n += gridDim.x, buf ^= 1) {
-    const T* x = static_cast<const T*>(P.x) + (long long)n * P.ldx;
-    const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg;
-    T* o = static_cast<T*>(P.o) + (long long)n * P.ldo;
-    Raw8<T> rx[kV], rg[kV];
+  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
+    fetch();
+    arrive();
+    f2 XA[4], XB[4], GA[4], GB[4], s = pk(0.f, 0.f), d = s;
+    {
+      f2 C[4], S[4], A[4], B[4];
+      angles_of(sm.cs[buf], l, C, S);
+      take(0, A, B);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      zero8(rx[j]);
-      zero8(rg[j]);
-      if (i < nvec) {
-        load8(rg[j], g + i * 8);
-        if (part < 2) load8(rx[j], x + i * 8);
+      for (int i = 0; i < 4; ++i) {
+        GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
+        GB[i] = fma2(B[i], C[i], neg2(mul2(A[i], S[i])));
+      }
+      take(2, XA, XB);
+      get_weights(weights, 0, A, B);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fma2(XB[i], XB[i], fma2(XA[i], XA[i], s));
+        d = fma2(XB[i], mul2(GB[i], B[i]), fma2(XA[i], mul2(GA[i], A[i]), d));
       }
     }
-    if (part == 2) {
+    from = depth == 2 ? stage - from : 0;
+    ang.ahead(a);  // the next token's angles, written ahead of the barrier
+    ang.put(sm.cs[buf ^ 1], tid, threads);
+    const float2 t = block_sum(make_float2(sum2(s), sum2(d)), sm, buf);
+    const float r = rsqrtf(t.x * inv + a.eps);
+    const float c = -t.y * inv * r * r * r;
+    const f2 rr = pk(r, r), cc = pk(c, c);
+    f2 WA[4], WB[4];
+    get_weights(weights, 0, WA, WB);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        const int i = j * blockDim.x + tid;
-        float f[8];
-        widen8(rg[j], f);
-        if (i < nvec) store8(o + i * 8, f);
-      }
-      continue;
+    for (int i = 0; i < 4; ++i) {
+      const f2 pA = mul2(GA[i], rr), pB = mul2(GB[i], rr);
+      accA[i] = fma2(pA, XA[i], accA[i]);
+      accB[i] = fma2(pB, XB[i], accB[i]);
+      GA[i] = fma2(pA, WA[i], mul2(XA[i], cc));
+      GB[i] = fma2(pB, WB[i], mul2(XB[i], cc));
     }
-    turn.load(a, n, -1.f);
-    float gn[kV][8], ss = 0.f, sd = 0.f;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      float xf[8], w[8];
-      widen8(rg[j], gn[j]);
-      turn.apply(gn[j]);
-      widen8(rx[j], xf);
-      param8(i < nvec ? P.w : nullptr, a.w_bf16, i * 8, 1.f, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(xf[e], xf[e], ss);
-        sd = fmaf(xf[e], gn[j][e] * w[e], sd);
-      }
-    }
-    const float2 s = block_sum(ss, sd, red, buf);
-    const float r = rsqrtf(s.x * inv + a.eps), c = s.y * inv * r * r;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      float xf[8], w[8], f[8];
-      widen8(rx[j], xf);
-      param8(i < nvec ? P.w : nullptr, a.w_bf16, i * 8, 1.f, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc[j][e] = fmaf(gn[j][e], xf[e] * r, acc[j][e]);
-        f[e] = r * (gn[j][e] * w[e] - xf[e] * c);
-      }
-      if (i < nvec) store8(o + i * 8, f);
-    }
+    if (on) pack16<kHalves>(o, l, GA, GB);
   }
-  if (part < 2 && P.part) {
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int i = j * blockDim.x + tid;
-      if (i < nvec) store8(P.part + (long long)blockIdx.x * nvec * 8 + i * 8, acc[j]);
-    }
-  }
+  if (P.part && on)
+    pack16<kHalves>(P.part + (long long)blockIdx.x * P.heads * a.d + h0, l, accA, accB);
 }
 
 // out[c] = sum over rows of part[row][c], for two matrices in one launch
@@ -509,16 +892,6 @@ __global__ void rope_table_kernel(TableArgs a) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    return 148;
-  }
-  return n;
-}
-
 struct RopeDims {
   long long tokens;
   int heads[2];       // q, k
@@ -576,9 +949,6 @@ basa_status check_rope(const basa_rope_params* p, bool bwd, RopeDims* r) {
   return BASA_OK;
 }
 
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 // Launch shape: CTAs along the tokens, and the chunks and steps of each part.
 struct RopeGrid {
   unsigned x, y;
@@ -588,33 +958,32 @@ struct RopeGrid {
 
 RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bool bwd) {
   RopeGrid g;
-  const int sms = sm_count();
+  const int sms = row_sm_count();
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
-    const int nvec = p->H * p->d / 8;  // H >= Hkv
-    g.v = nvec <= 128 ? 1 : 4;
-    g.threads = ((nvec + g.v - 1) / g.v + 31) / 32 * 32;
+    const int units = p->H * p->d / 16;  // H >= Hkv
+    g.v = bwd || units <= 64 ? 1 : 2;
+    g.threads = ((units + g.v - 1) / g.v + 31) / 32 * 32;
     g.chunks[0] = g.chunks[1] = 1;
     g.steps[0] = g.steps[1] = 0;
     g.y = with_v ? 3 : 2;
-    const int per_sm = (bwd ? 640 : 1024) / g.threads;
+    const int per_sm = (bwd ? 640 : 640) / g.threads;
     const long long cap = (long long)sms * (per_sm > 1 ? per_sm : 1);
     g.x = (unsigned)(r.tokens < cap ? r.tokens : cap);
     return g;
   }
-  const int hpw = 32 / (p->d / 8);
-  const int batch = bwd ? kRopeBwdBatch : kRopeBatch;
+  const int hpw = 512 / p->d;
   g.threads = kRopeThreads;
   g.v = 0;
   g.y = 0;
   for (int i = 0; i < 2; ++i) {
     const int steps = (r.heads[i] + hpw - 1) / hpw;
-    const int want = (steps + 3 * batch - 1) / (3 * batch);
-    g.steps[i] = ((steps + want - 1) / want + batch - 1) / batch * batch;
+    const int want = (steps + 7) / 8;
+    g.steps[i] = ((steps + want - 1) / want + 1) / 2 * 2;
     g.chunks[i] = (steps + g.steps[i] - 1) / g.steps[i];
   }
   g.y = g.chunks[0] + g.chunks[1] + (with_v ? g.chunks[1] : 0);
   const long long need = (r.tokens + kRopeWarps - 1) / kRopeWarps;
-  const long long cap = (long long)sms * (bwd ? 4 : 16);
+  const long long cap = (long long)sms * (bwd ? 8 : 32);
   g.x = (unsigned)(need < cap ? need : cap);
   return g;
 }
@@ -640,37 +1009,55 @@ void go_head_bwd(const RopeGrid& g, const RopeArgs& a, bool halves, bool norm, c
   else if (norm) rope_head_bwd_kernel<T, kLph, false, true><<<grid, kRopeThreads, 0, st>>>(a);
   else rope_head_bwd_kernel<T, kLph, false, false><<<grid, kRopeThreads, 0, st>>>(a);
 }
+// Dynamic shared memory beyond what a kernel may use unasked has to be allowed.
+template <typename K>
+bool allow(K kernel, int smem) {
+  return smem <= 32 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+             cudaSuccess;
+}
+template <typename K, typename... Args>
+bool go_token(K kernel, const RopeGrid& g, int smem, cudaStream_t st, const Args&... args) {
+  if (!allow(kernel, smem)) return false;
+  kernel<<<dim3(g.x, g.y), g.threads, smem, st>>>(args...);
+  return true;
+}
 template <typename TI, typename TO>
-void go_fwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
+bool go_fwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
   const bool halves = p->layout == BASA_ROPE_HALVES;
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
-    const dim3 grid(g.x, g.y);
-    if (g.v == 1 && halves) rope_token_kernel<TI, TO, 1, true><<<grid, g.threads, 0, st>>>(a);
-    else if (g.v == 1) rope_token_kernel<TI, TO, 1, false><<<grid, g.threads, 0, st>>>(a);
-    else if (halves) rope_token_kernel<TI, TO, 4, true><<<grid, g.threads, 0, st>>>(a);
-    else rope_token_kernel<TI, TO, 4, false><<<grid, g.threads, 0, st>>>(a);
-    return;
+    const int smem =
+        weight_bytes(g.v, g.threads) + kStages<TI> * Slot<TI>::bytes(2 * g.v, g.threads);
+    if (g.v == 1)
+      return halves ? go_token(rope_token_kernel<TI, TO, 1, true>, g, smem, st, a)
+                    : go_token(rope_token_kernel<TI, TO, 1, false>, g, smem, st, a);
+    return halves ? go_token(rope_token_kernel<TI, TO, 2, true>, g, smem, st, a)
+                  : go_token(rope_token_kernel<TI, TO, 2, false>, g, smem, st, a);
   }
   const bool norm = p->norm != BASA_ROPE_NORM_NONE;
-  if (p->d == 128) go_head<TI, TO, 16>(g, a, halves, norm, st);
-  else if (p->d == 64) go_head<TI, TO, 8>(g, a, halves, norm, st);
-  else go_head<TI, TO, 4>(g, a, halves, norm, st);
+  if (p->d == 128) go_head<TI, TO, 8>(g, a, halves, norm, st);
+  else if (p->d == 64) go_head<TI, TO, 4>(g, a, halves, norm, st);
+  else go_head<TI, TO, 2>(g, a, halves, norm, st);
+  return true;
 }
 template <typename T>
-void go_bwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
+bool go_bwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
   const bool halves = p->layout == BASA_ROPE_HALVES;
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
-    const dim3 grid(g.x, g.y);
-    if (g.v == 1 && halves) rope_token_bwd_kernel<T, 1, true><<<grid, g.threads, 0, st>>>(a);
-    else if (g.v == 1) rope_token_bwd_kernel<T, 1, false><<<grid, g.threads, 0, st>>>(a);
-    else if (halves) rope_token_bwd_kernel<T, 4, true><<<grid, g.threads, 0, st>>>(a);
-    else rope_token_bwd_kernel<T, 4, false><<<grid, g.threads, 0, st>>>(a);
-    return;
+    const int w = weight_bytes(1, g.threads), stage = Slot<T>::bytes(4, g.threads);
+    const int depth = w + 2 * stage <= 220 * 1024 ? 2 : 1;  // fp32 rows of over 11 K values: 1
+    const int smem = w + depth * stage;
+    if (g.threads <= 320)
+      return halves ? go_token(rope_token_bwd_kernel<T, 320, 2, true>, g, smem, st, a, depth)
+                    : go_token(rope_token_bwd_kernel<T, 320, 2, false>, g, smem, st, a, depth);
+    return halves ? go_token(rope_token_bwd_kernel<T, 1024, 1, true>, g, smem, st, a, depth)
+                  : go_token(rope_token_bwd_kernel<T, 1024, 1, false>, g, smem, st, a, depth);
   }
   const bool norm = p->norm != BASA_ROPE_NORM_NONE;
-  if (p->d == 128) go_head_bwd<T, 16>(g, a, halves, norm, st);
-  else if (p->d == 64) go_head_bwd<T, 8>(g, a, halves, norm, st);
-  else go_head_bwd<T, 4>(g, a, halves, norm, st);
+  if (p->d == 128) go_head_bwd<T, 8>(g, a, halves, norm, st);
+  else if (p->d == 64) go_head_bwd<T, 4>(g, a, halves, norm, st);
+  else go_head_bwd<T, 2>(g, a, halves, norm, st);
+  return true;
 }
 
 RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid& g,
@@ -761,14 +1148,13 @@ basa_status basa_qkv_rope(const void* q, const void* k, const void* v, const voi
   a.q.w = q_weight; a.k.w = k_weight;
   a.q.o = q_out; a.k.o = k_out; a.v.o = v_out;
   const bool low = p->out_dtype == BASA_FP8_E4M3;
-  if (p->dtype == BASA_BF16) {
-    if (low) go_fwd<__nv_bfloat16, e4m3_t>(p, g, a, stream);
-    else go_fwd<__nv_bfloat16, __nv_bfloat16>(p, g, a, stream);
-  } else {
-    if (low) go_fwd<float, e4m3_t>(p, g, a, stream);
-    else go_fwd<float, float>(p, g, a, stream);
-  }
-  return launched();
+  const bool ok = p->dtype == BASA_BF16
+                      ? (low ? go_fwd<__nv_bfloat16, e4m3_t>(p, g, a, stream)
+                             : go_fwd<__nv_bfloat16, __nv_bfloat16>(p, g, a, stream))
+                      : (low ? go_fwd<float, e4m3_t>(p, g, a, stream)
+                             : go_fwd<float, float>(p, g, a, stream));
+  const basa_status l = launched();
+  return ok ? l : BASA_ERR_CUDA;
 }
 
 size_t basa_qkv_rope_bwd_workspace_size(const basa_rope_params* p) {
@@ -824,10 +1210,9 @@ basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void
   char* ws = static_cast<char*>(workspace);
   if (dq_weight) a.q.part = reinterpret_cast<float*>(ws);
   if (dk_weight) a.k.part = reinterpret_cast<float*>(ws + rope_part_bytes(p, r, g, 0));
-  if (p->dtype == BASA_BF16)
-    go_bwd<__nv_bfloat16>(p, g, a, stream);
-  else
-    go_bwd<float>(p, g, a, stream);
+  const bool ok = p->dtype == BASA_BF16 ? go_bwd<__nv_bfloat16>(p, g, a, stream)
+                                        : go_bwd<float>(p, g, a, stream);
+  if ((s = launched()) != BASA_OK || !ok) return BASA_ERR_CUDA;
   if (sums) {
     const ColSum c0{a.q.part, dq_weight, (int)g.x * g.chunks[0], cols[0]};
     const ColSum c1{a.k.part, dk_weight, (int)g.x * g.chunks[1], cols[1]};

@@ -1,7 +1,7 @@
 // Device helpers shared by the kernels that walk token rows (basa_rope.cu,
-// basa_gnorm.cu): eight consecutive elements of a row as one unit of loading,
-// widening, narrowing and storing, sums over a warp, and the column sums that
-// end a weight's gradient.  Everything here has internal linkage.
+// basa_gnorm.cu): eight consecutive elements of a row as one unit of loading and
+// storing, packed fp32 pairs as the unit of arithmetic, parameters of two types.
+// Everything here has internal linkage.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,12 +12,51 @@
 namespace basa {
 namespace {
 
+// ---------------------------------------------------------------------------
+// Packed fp32 pairs (sm_100's f32x2 arithmetic): two values an instruction.
+// These kernels move about 24 bytes per SM and clock, so the instructions spent
+// per value decide whether they keep up with HBM.
+// ---------------------------------------------------------------------------
+typedef uint64_t f2;
+
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 un(f2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 f = un(v);
+  return f.x + f.y;
+}
+
+// ---------------------------------------------------------------------------
+// Eight consecutive elements
+// ---------------------------------------------------------------------------
 struct e4m3_t {
   uint8_t bits;
 };
 
-// Eight consecutive elements as they lie in memory.
-template <typename T> struct Raw8;
+template <typename T> struct Raw8;  // as they lie in memory
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
 template <> struct Raw8<float> { uint4 a, b; };
 
@@ -31,19 +70,22 @@ __device__ __forceinline__ void load8(Raw8<float>& r, const float* p) {
 __device__ __forceinline__ void zero8(Raw8<__nv_bfloat16>& r) { r.a = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void zero8(Raw8<float>& r) { r.a = r.b = make_uint4(0, 0, 0, 0); }
 
-// Exact: a bf16 value is the upper half of the fp32 value it stands for.
-__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16>& r, float (&f)[8]) {
-  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Element i of the eight, in fp32.  Exact: a bf16 value is the upper half of
+// the fp32 value it stands for.
+__device__ __forceinline__ float elem(const Raw8<__nv_bfloat16>& r, int i) {
+  const uint32_t w = i < 2 ? r.a.x : i < 4 ? r.a.y : i < 6 ? r.a.z : r.a.w;
+  return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
 }
-__device__ __forceinline__ void widen8(const Raw8<float>& r, float (&f)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+__device__ __forceinline__ float elem(const Raw8<float>& r, int i) {
+  const uint4& v = i < 4 ? r.a : r.b;
+  const int k = i & 3;
+  return __uint_as_float(k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w);
+}
+// In order: p[i] = (element 2i, element 2i + 1).
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, f2 (&p)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  for (int i = 0; i < 4; ++i) p[i] = pk(elem(r, 2 * i), elem(r, 2 * i + 1));
 }
 
 // Rounds to nearest even, once, on the way out.
@@ -72,9 +114,65 @@ __device__ __forceinline__ void store8(e4m3_t* p, const float (&f)[8]) {
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
+template <typename T>
+__device__ __forceinline__ void store8(T* o, const f2 (&p)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = un(p[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+  store8(o, f);
+}
 
-// Eight parameters (norm weights, modulations) of type bf16 or fp32 from
+// ---------------------------------------------------------------------------
+// Asynchronous copies.  Every thread copies its own columns of a row to its own
+// bytes of a stage in shared memory and is the only one to read them, so the
+// stages need no barrier.  A slot holds one tensor's vectors of a stage, in
+// 16-byte pieces, the threads side by side.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most kAhead of this thread's groups are in flight.
+template <int kAhead>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+}
+
+template <typename T>
+struct Slot {
+  static constexpr int kPieces = (int)sizeof(T) / 2;
+  __host__ __device__ static constexpr int bytes(int vectors, int threads) {
+    return vectors * kPieces * threads * 16;
+  }
+  __device__ static __forceinline__ void fetch(uint32_t at, const T* src, int j, int threads,
+                                               int tid) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      copy16(at + ((j * kPieces + p) * threads + tid) * 16,
+             reinterpret_cast<const char*>(src) + p * 16);
+  }
+  __device__ static __forceinline__ void take(const char* at, int j, int threads, int tid,
+                                              Raw8<T>& r) {
+    const uint4* s = reinterpret_cast<const uint4*>(at) + j * kPieces * threads + tid;
+    r.a = s[0];
+    if constexpr (kPieces == 2) r.b = s[threads];
+  }
+};
+
+__device__ __forceinline__ uint32_t shared_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---------------------------------------------------------------------------
+// Parameters (norm weights, modulations) of type bf16 or fp32, eight from
 // column `col`, a multiple of 8; `fill` where there are none.
+// ---------------------------------------------------------------------------
 __device__ __forceinline__ void param8(const void* p, bool bf16, long long col, float fill,
                                        float (&f)[8]) {
   if (!p) {
@@ -83,18 +181,26 @@ __device__ __forceinline__ void param8(const void* p, bool bf16, long long col, 
   } else if (bf16) {
     Raw8<__nv_bfloat16> r;
     r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + col));
-    widen8(r, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = elem(r, i);
   } else {
     Raw8<float> r;
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + col);
     r.a = __ldg(q);
     r.b = __ldg(q + 1);
-    widen8(r, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = elem(r, i);
   }
 }
-// Eight gradients of parameters, in the parameters' type.
-__device__ __forceinline__ void store_param8(void* p, bool bf16, long long col,
-                                             const float (&f)[8]) {
+__device__ __forceinline__ void param8(const void* p, bool bf16, long long col, float fill,
+                                       f2 (&v)[4]) {
+  float f[8];
+  param8(p, bf16, col, fill, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
+}
+// Gradients of parameters, in the parameters' type.
+__device__ __forceinline__ void store_param8(void* p, bool bf16, long long col, const f2 (&f)[4]) {
   if (bf16)
     store8(static_cast<__nv_bfloat16*>(p) + col, f);
   else
@@ -113,6 +219,32 @@ __device__ __forceinline__ float lane_sum(float v) {
   for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Two sums side by side.
+template <int kLanes>
+__device__ __forceinline__ float2 lane_sum(float2 v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v.x, o), y = __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.x += x;
+    v.y += y;
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+inline int row_sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();  // no device: the workspace sizes of a B200
+    return 148;
+  }
+  return n;
+}
+inline bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 }  // namespace basa

@@ -129,6 +129,7 @@ ROPE = [
     (1, (4, 6, 5), 9, 3, 64, (2, 10, 20), "head", "halves", BF, BF, BF, True, 8),
     (1, (2, 6, 5), 40, 40, 128, (44, 42, 42), "token", "pairs", BF, BF, BF, False, 9),
     (1, (1, 6, 5), 128, 8, 128, (0, 64, 64), "token", "halves", BF, BF, BF, False, 10),
+    (1, (1, 6, 5), 128, 128, 128, (0, 64, 64), "token", "pairs", F32, F32, F32, False, 19),
     (1, (1, 4, 7), 4, 4, 128, (0, 0, 0), "head", "pairs", BF, BF, F32, True, 11),
     (1, (1, 4, 7), 4, 2, 64, (0, 20, 44), None, "pairs", BF, BF, None, True, 12),
     (2, (2, 3, 5), 7, 7, 128, (32, 48, 48), None, "halves", F32, F32, None, False, 13),
