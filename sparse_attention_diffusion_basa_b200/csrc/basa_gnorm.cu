@@ -43,8 +43,12 @@ struct GnArgs {
   int norm, post;
   float eps, post_eps, res, inv;
   int mod_bf16, w_bf16;
-  int depth;                // stages of the read-ahead ring
+  int depth;                // stages of a read-ahead ring
   int need_y;
+  // forward: warps that share a row, rows a CTA works on at a time
+  int warps, teams;
+  int direct;               // every team keeps the factors of its own row
+  int wide;                 // fp32 outputs are aligned to 32 bytes
 };
 
 // Waits until at most depth - 1 of this thread's copies are in flight.
@@ -56,231 +60,411 @@ __device__ __forceinline__ void ring_wait(int depth) {
   else
     copy_wait<0>();
 }
-template <typename T>
-__device__ __forceinline__ void take(const char* at, int j, f2 (&f)[4]) {
-  Raw8<T> r;
-  Slot<T>::take(at, j, blockDim.x, threadIdx.x, r);
-  widen8(r, f);
-}
+__device__ __forceinline__ f2 both(float v) { return pk(v, v); }
 
 // ---------------------------------------------------------------------------
-// Sums over a row.  Every warp leaves its part in shared memory and, behind one
-// barrier, adds up all warps' parts itself, one a lane.  `buf` alternates from
-// sum to sum, so that barrier is the only one.
+// Sums over a row that a team of warps holds.  Every warp leaves its part in
+// shared memory and, behind the team's barrier, adds up all parts in order.
+// `buf` alternates from sum to sum, so that barrier is the only one.
 // ---------------------------------------------------------------------------
-struct RowSmem {
-  float2 red[2][kMaxWarps];
+struct Team {
+  int warps, id;      // of this team
+  int threads, tid;   // threads of the team, and this one's number among them
+  int lane, warp;     // warp: its number in the team
+  float4 (*red)[kMaxWarps];  // [2][warps of the CTA], at this team's first warp
+  int buf;
+
+  __device__ __forceinline__ void sync() const {
+    if (warps == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+  }
+  __device__ __forceinline__ const float4* share(float4 v) {
+    float4* at = reinterpret_cast<float4*>(red[buf]);
+    buf ^= 1;
+    if (lane == 0) at[warp] = v;
+    sync();
+    return at;
+  }
+  // Two sums of one row, or of each of two rows.
+  __device__ __forceinline__ void sums(const float2 (&v)[1], float2 (&s)[1]) {
+    const float2 w = lane_sum<32>(v[0]);
+    const float4* p = share(make_float4(w.x, w.y, 0.f, 0.f));
+    s[0] = make_float2(0.f, 0.f);
+    for (int i = 0; i < warps; ++i) {
+      const float2 u = *reinterpret_cast<const float2*>(p + i);
+      s[0].x += u.x;
+      s[0].y += u.y;
+    }
+  }
+  __device__ __forceinline__ void sums(const float2 (&v)[2], float2 (&s)[2]) {
+    float4 w = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      w.x += __shfl_xor_sync(0xffffffffu, w.x, o);
+      w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
+      w.z += __shfl_xor_sync(0xffffffffu, w.z, o);
+      w.w += __shfl_xor_sync(0xffffffffu, w.w, o);
+    }
+    const float4* p = share(w);
+    s[0] = s[1] = make_float2(0.f, 0.f);
+    for (int i = 0; i < warps; ++i) {
+      const float4 u = p[i];
+      s[0].x += u.x;
+      s[0].y += u.y;
+      s[1].x += u.z;
+      s[1].y += u.w;
+    }
+  }
 };
 
-__device__ __forceinline__ float2 share(float2 v, RowSmem& sm, int& buf) {
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) sm.red[buf][threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < (int)(blockDim.x >> 5) ? sm.red[buf][lane] : make_float2(0.f, 0.f);
-  buf ^= 1;
-  return v;
-}
-
-__device__ __forceinline__ float2 row_sum2(f2 a, f2 b, RowSmem& sm, int& buf) {
-  const float2 v = lane_sum<32>(make_float2(sum2(a), sum2(b)));
-  return lane_sum<32>(share(v, sm, buf));
-}
-
-// Elements of a row that warp i holds.
-__device__ __forceinline__ float warp_elements(int i, int kv, int nvec) {
+// Elements of a row in this warp.
+__device__ __forceinline__ float elements_of(const Team& t, int kv, int nvec) {
   int n = 0;
   for (int j = 0; j < kv; ++j) {
-    const int left = nvec - j * (int)blockDim.x - 32 * i;
+    const int left = nvec - j * t.threads - 32 * t.warp;
     n += left < 0 ? 0 : left > 32 ? 32 : left;
   }
   return (float)(8 * n);
 }
 
-struct Counts {      // elements of a warp: of this thread's, and of warp number `lane`
-  float inv_mine;    // 1 / elements, 0 where there are none
-  float lanes, inv_lanes;
-};
-
 // (mean, rstd) of a row held kV * 8 values a thread, zeros where ok is false.
 // Layer: the squares are taken about each warp's own mean and joined about the
 // row's (Chan, Golub and LeVeque's update), so a mean far from zero costs no
-// digits and one barrier is enough.
+// digits and one barrier is enough.  n, inv_n: elements of the warp.
 template <int kV>
 __device__ __forceinline__ float2 row_stats(const f2 (&f)[kV][4], const bool (&ok)[kV], int kind,
-                                            float eps, float inv, const Counts& n, RowSmem& sm,
-                                            int& buf) {
-  f2 q = pk(0.f, 0.f);
+                                            float eps, float inv, float n, float inv_n, Team& t) {
+  f2 q0 = 0, q1 = 0;
   if (kind == BASA_NORM_LAYER) {
-    f2 t = pk(0.f, 0.f);
+    f2 s0 = 0, s1 = 0;
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t = add2(t, f[j][i]);
-    const float s = lane_sum<32>(sum2(t));
-    const float m = -s * n.inv_mine;
-    const f2 mm = pk(m, m);
+      for (int i = 0; i < 4; i += 2) {
+        s0 = add2(s0, f[j][i]);
+        s1 = add2(s1, f[j][i + 1]);
+      }
+    const float m = lane_sum<32>(sum2(add2(s0, s1))) * inv_n;
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
-      if (ok[j])
+    for (int j = 0; j < kV; ++j) {
+      const f2 mm = both(ok[j] ? -m : 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f2 d = add2(f[j][i], mm);
-          q = fma2(d, d, q);
-        }
-    const float2 v = share(make_float2(s, lane_sum<32>(sum2(q))), sm, buf);
-    const float mean = lane_sum<32>(v.x) * inv;
-    const float d = v.x * n.inv_lanes - mean;
-    const float m2 = lane_sum<32>(fmaf(n.lanes * d, d, v.y));
+      for (int i = 0; i < 4; i += 2) {
+        const f2 a = add2(f[j][i], mm), b = add2(f[j][i + 1], mm);
+        q0 = fma2(a, a, q0);
+        q1 = fma2(b, b, q1);
+      }
+    }
+    const float q = lane_sum<32>(sum2(add2(q0, q1)));
+    const float4* p = t.share(make_float4(m, q, n, 0.f));
+    float mean = 0.f, m2 = 0.f;
+    for (int i = 0; i < t.warps; ++i) mean = fmaf(p[i].x, p[i].z, mean);
+    mean *= inv;
+    for (int i = 0; i < t.warps; ++i) {
+      const float4 w = p[i];
+      const float d = w.x - mean;
+      m2 += fmaf(w.z * d, d, w.y);
+    }
     return make_float2(mean, rsqrtf(m2 * inv + eps));
   }
 #pragma unroll
   for (int j = 0; j < kV; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q = fma2(f[j][i], f[j][i], q);
-  const float2 v = share(make_float2(0.f, lane_sum<32>(sum2(q))), sm, buf);
-  return make_float2(0.f, rsqrtf(lane_sum<32>(v.y) * inv + eps));
+    for (int i = 0; i < 4; i += 2) {
+      q0 = fma2(f[j][i], f[j][i], q0);
+      q1 = fma2(f[j][i + 1], f[j][i + 1], q1);
+    }
+  const float4* p = t.share(make_float4(lane_sum<32>(sum2(add2(q0, q1))), 0.f, 0.f, 0.f));
+  float q = 0.f;
+  for (int i = 0; i < t.warps; ++i) q += p[i].x;
+  return make_float2(0.f, rsqrtf(q * inv + eps));
 }
 
-__device__ __forceinline__ f2 both(float v) { return pk(v, v); }
+// A modulation row's factors for the eight columns from `col`: gate * pw of the
+// branch; (1 + scale) * w and (1 + scale) * b + shift of the norm.
+__device__ __forceinline__ void gate8(const GnArgs& a, long long g, int col, f2 (&G)[4]) {
+  f2 p[4];
+  param8(a.gate, a.mod_bf16, g * a.ld_gate + col, 1.f, G);
+  if (a.pw) {
+    param8(a.pw, a.w_bf16, col, 1.f, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) G[i] = mul2(G[i], p[i]);
+  }
+}
+__device__ __forceinline__ void scale8(const GnArgs& a, long long g, int col, f2 (&S)[4],
+                                       f2 (&p)[4]) {
+  param8(a.scale, a.mod_bf16, g * a.ld_scale + col, 0.f, p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) S[i] = p[i] = add2(p[i], both(1.f));
+  if (a.w) {
+    f2 w[4];
+    param8(a.w, a.w_bf16, col, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[i] = mul2(S[i], w[i]);
+  }
+}
+__device__ __forceinline__ void affine8(const GnArgs& a, long long g, int col, f2 (&S)[4],
+                                        f2 (&B)[4]) {
+  f2 p[4];
+  scale8(a, g, col, S, p);
+  param8(a.shift, a.mod_bf16, g * a.ld_shift + col, 0.f, B);
+  if (a.b) {
+    f2 b[4];
+    param8(a.b, a.w_bf16, col, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) B[i] = fma2(b[i], p[i], B[i]);
+  }
+}
+// An array of fp32 factors in shared memory: two 16-byte pieces of a vector, the
+// first pieces of all vectors and then the second ones, `half` bytes further.
+// One more vector of zeros stands for all vectors past the row's end.
+__host__ __device__ constexpr int factor_half(int nvec) { return (nvec + 1) * 16; }
+__device__ __forceinline__ void put8(char* at, int half, const f2 (&f)[4]) {
+  *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f[0], f[1]);
+  *reinterpret_cast<ulonglong2*>(at + half) = make_ulonglong2(f[2], f[3]);
+}
+__device__ __forceinline__ void get8(const char* at, int half, f2 (&f)[4]) {
+  const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(at),
+                   y = *reinterpret_cast<const ulonglong2*>(at + half);
+  f[0] = x.x;
+  f[1] = x.y;
+  f[2] = y.x;
+  f[3] = y.y;
+}
+// A thread's columns of a row: vector j of eight at col[j], whether it is inside
+// the row, and where its factors lie.  Vectors past the row's end are filled
+// with zeros on the way in, have factors of zero, are computed with like the
+// others (to zeros) and not stored, so the loops over a thread's vectors have no
+// branches.
+template <int kV>
+struct Cols {
+  int col[kV], at[kV];
+  bool ok[kV];
+  __device__ __forceinline__ void init(const Team& t, int nvec) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int v = j * t.threads + t.tid;
+      ok[j] = v < nvec;
+      col[j] = ok[j] ? v * 8 : 0;
+      at[j] = (ok[j] ? v : nvec) * 16;
+    }
+  }
+};
+
+// One tensor's part of a ring stage: for each vector of a thread and each warp,
+// the warp's 512 bytes (fp32: 1 KB) as they lie in memory.  bf16: a lane copies
+// its own vector.  fp32: a vector is two 16-byte pieces; the lanes copy
+// consecutive pieces, not their own, so that a request covers whole lines (with
+// a lane's own pieces, 32 bytes apart, the L2 sees one request for each piece).
+template <typename T, int kV>
+struct Part {
+  static constexpr int kPieces = (int)sizeof(T) / 2;
+  int col[kV][kPieces];      // element the lane copies from
+  uint32_t size[kV][kPieces];  // 16, or 0: zeros
+  uint32_t to;               // offset of this warp's first piece of this lane
+  uint32_t step;             // from vector to vector
+  __device__ __forceinline__ void init(const Team& t, int nvec) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const int piece = p * 32 + t.lane;  // of the warp's pieces in memory order
+        const int v = j * t.threads + t.warp * 32 + piece / kPieces;
+        col[j][p] = v < nvec ? v * 8 + (piece % kPieces) * 4 : 0;
+        size[j][p] = v < nvec ? 16 : 0;
+      }
+    to = t.warp * kPieces * 512 + t.lane * 16;
+    step = t.warps * kPieces * 512;
+  }
+  static __host__ __device__ constexpr int bytes(int threads) {
+    return kV * threads * kPieces * 16;
+  }
+  __device__ __forceinline__ void fetch(uint32_t at, const T* row, bool on = true) const {
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         at + to + j * step + p * 512),
+                     "l"(row + (on ? col[j][p] : 0)), "r"(on ? size[j][p] : 0u)
+                     : "memory");
+  }
+  __device__ __forceinline__ static void take(const char* at, int j, const Team& t, f2 (&f)[4]) {
+    const uint4* s =
+        reinterpret_cast<const uint4*>(at) + ((j * t.warps + t.warp) * 32 + t.lane) * kPieces;
+    Raw8<T> r;
+    r.a = s[0];
+    if constexpr (kPieces == 2) r.b = s[1];
+    widen8(r, f);
+  }
+};
+
+__device__ __forceinline__ void put_row(__nv_bfloat16* p, const f2 (&f)[4], bool) { store8(p, f); }
+// fp32: 32 bytes a lane in one store where the tensor is aligned to them, so
+// that no request writes half a sector.
+__device__ __forceinline__ void put_row(float* p, const f2 (&f)[4], bool wide) {
+  if (wide)
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(f[0]), "l"(f[1]),
+                 "l"(f[2]), "l"(f[3])
+                 : "memory");
+  else
+    store8(p, f);
+}
 
 // ---------------------------------------------------------------------------
-// Forward
+// Forward.  One CTA an SM takes a contiguous range of rows, `teams` rows at a
+// time, each in the registers of one team of warps: a row's own sums are a chain
+// of exchanges that several rows at a time hide.  The factors of a modulation
+// row are combined once, in fp32, into shared memory for all the teams (direct:
+// a modulation covers too few rows for that, and each team keeps its own).
 // ---------------------------------------------------------------------------
-template <typename TX, typename TY, int kV, int kThreads, int kCtas, bool kBranch, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kCtas) gnorm_kernel(GnArgs a) {
-  extern __shared__ __align__(16) char ring[];
-  __shared__ RowSmem sm;
-  const int tid = threadIdx.x, threads = blockDim.x, nvec = a.C / 8;
-  bool ok[kV];
-#pragma unroll
-  for (int j = 0; j < kV; ++j) ok[j] = j * threads + tid < nvec;
-  const int next = threads * 8;  // columns from one of a thread's vectors to the next
-  Counts cnt;
-  {
-    const float mine = warp_elements(tid >> 5, kV, nvec);
-    cnt.inv_mine = mine > 0.f ? 1.f / mine : 0.f;
-    cnt.lanes = (tid & 31) < (threads >> 5) ? warp_elements(tid & 31, kV, nvec) : 0.f;
-    cnt.inv_lanes = cnt.lanes > 0.f ? 1.f / cnt.lanes : 0.f;
-  }
-  const int x_bytes = Slot<TX>::bytes(kV, threads);
-  const int stage = x_bytes + (kBranch ? Slot<TY>::bytes(kV, threads) : 0);
+constexpr int kFwdThreads = 640;
+
+template <typename TX, typename TY, int kV, bool kBranch, bool kNorm>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    gnorm_kernel(const __grid_constant__ GnArgs a) {
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ float4 red[2][kMaxWarps];
+  const int nvec = a.C / 8;
+  Team t;
+  t.warps = a.warps;
+  t.lane = threadIdx.x & 31;
+  t.id = (threadIdx.x >> 5) / t.warps;
+  t.warp = (threadIdx.x >> 5) - t.id * t.warps;
+  t.threads = 32 * t.warps;
+  t.tid = 32 * t.warp + t.lane;
+  t.red = reinterpret_cast<float4(*)[kMaxWarps]>(&red[0][t.id * t.warps]);
+  t.buf = 0;
+  Cols<kV> c;
+  c.init(t, nvec);
+  Part<TX, kV> px;
+  Part<TY, kV> py;
+  px.init(t, nvec);
+  if (kBranch) py.init(t, nvec);
+  const float n = elements_of(t, kV, nvec), inv_n = n > 0.f ? 1.f / n : 0.f;
+  const int half = factor_half(nvec), arr = 2 * half;  // bytes of one array of factors
+  const int factors = ((kBranch ? 1 : 0) + (kNorm ? 2 : 0)) * arr;
+  char* const sG = dyn + (a.direct ? t.id * factors : 0);
+  char* const sS = sG + (kBranch ? arr : 0);
+  char* const sB = sS + (kNorm ? arr : 0);
+  const int x_bytes = Part<TX, kV>::bytes(t.threads);
+  const int stage = x_bytes + (kBranch ? Part<TY, kV>::bytes(t.threads) : 0);
+  char* const ring = dyn + (a.direct ? a.teams : 1) * factors + t.id * a.depth * stage;
+  const uint32_t ring_at = shared_u32(ring);
   const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
   const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
-  const long long off = (long long)r0 * a.C + tid * 8;
+  const long long off = (long long)(r0 + t.id) * a.C, skip = (long long)a.teams * a.C;
   const TX* x = static_cast<const TX*>(a.x) + off;
   const TY* y = kBranch ? static_cast<const TY*>(a.y) + off : nullptr;
   TX* xo = kBranch ? static_cast<TX*>(a.xo) + off : nullptr;
   TY* h = kNorm ? static_cast<TY*>(a.h) + off : nullptr;
-  const uint32_t ring_at = shared_u32(ring);
-  int ahead = 0, to_stage = 0;  // rows asked for, and the stage of the next
-  auto fetch = [&]() {
-    if (r0 + ahead < r1) {
-      const uint32_t at = ring_at + to_stage;
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
-          Slot<TX>::fetch(at, x + j * next, j, threads, tid);
-          if (kBranch) Slot<TY>::fetch(at + x_bytes, y + j * next, j, threads, tid);
-        }
-      x += a.C;
-      if (kBranch) y += a.C;
+  int ahead = r0 + t.id, at_stage = 0;
+  auto fetch = [&](int to) {
+    __syncwarp();  // every lane has read what the stage held
+    if (ahead < r1) {
+      px.fetch(ring_at + to, x);
+      x += skip;
+      if (kBranch) {
+        py.fetch(ring_at + to + x_bytes, y);
+        y += skip;
+      }
+      ahead += a.teams;
     }
     copy_commit();
-    ++ahead;
-    to_stage = to_stage + stage == a.depth * stage ? 0 : to_stage + stage;
   };
-  for (int s = 0; s < a.depth - 1; ++s) fetch();
-  f2 G[kV][4], S[kV][4], B[kV][4];
-  long long g_end = r0;
-  int buf = 0, at_stage = 0;
-  for (int r = r0; r < r1; ++r) {
-    fetch();
-    if (r >= g_end) {  // another modulation row
-      const long long g = r / a.group;
-      g_end = (g + 1) * a.group;
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        const long long c = ok[j] ? tid * 8 + j * next : 0;
-        f2 p[4], q[4];
-        if (kBranch) {
-          param8(a.gate, a.mod_bf16, g * a.ld_gate + c, 1.f, G[j]);
-          param8(a.pw, a.w_bf16, c, 1.f, p);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) G[j][i] = mul2(G[j][i], p[i]);
-        }
-        if (kNorm) {
-          param8(a.scale, a.mod_bf16, g * a.ld_scale + c, 0.f, p);
-          param8(a.w, a.w_bf16, c, 1.f, S[j]);
-          param8(a.b, a.w_bf16, c, 0.f, B[j]);
-          param8(a.shift, a.mod_bf16, g * a.ld_shift + c, 0.f, q);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = add2(p[i], both(1.f));
-            S[j][i] = mul2(S[j][i], p[i]);
-            B[j][i] = fma2(B[j][i], p[i], q[i]);
-          }
-        }
-      }
-    }
-    ring_wait(a.depth);
-    const char* at = ring + at_stage;
-    at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
-    f2 f[kV][4];
-    float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[j][i] = 0;
+  auto fill = [&](long long g, int v) {
+    f2 S[4] = {0, 0, 0, 0}, B[4] = {0, 0, 0, 0};
     if (kBranch) {
-      f2 u[kV][4];
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[j][i] = 0;
-        if (ok[j]) take<TY>(at + x_bytes, j, u[j]);
-      }
-      if (a.post != BASA_NORM_NONE) {
-        post = row_stats<kV>(u, ok, a.post, a.post_eps, a.inv, cnt, sm, buf);
-        const f2 m = both(-post.x), s = both(post.y);
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[j][i] = mul2(add2(u[j][i], m), s);
-      }
-      const f2 res = both(a.res);
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
-          take<TX>(at, j, f[j]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[j][i] = fma2(res, f[j][i], mul2(u[j][i], G[j][i]));
-          store8(xo + j * next, f[j]);
-        }
-      xo += a.C;
-    } else {
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) take<TX>(at, j, f[j]);
+      if (v < nvec) gate8(a, g, v * 8, S);
+      put8(sG + v * 16, half, S);
     }
     if (kNorm) {
-      pre = row_stats<kV>(f, ok, a.norm, a.eps, a.inv, cnt, sm, buf);
-      const f2 m = both(-pre.x), s = both(pre.y);
+      if (v < nvec) affine8(a, g, v * 8, S, B);
+      put8(sS + v * 16, half, S);
+      put8(sB + v * 16, half, B);
+    }
+  };
+  for (int s = 0; s < a.depth; ++s) fetch(s * stage);
+  int r = r0 + t.id;
+  for (int seg = r0; seg < r1;) {  // rows of one modulation, or, direct, all rows
+    long long g = seg / a.group;
+    int end = r1;
+    if (!a.direct) {
+      end = (int)min((long long)r1, (g + 1) * a.group);
+      __syncthreads();
+      for (int v = threadIdx.x; v <= nvec; v += blockDim.x) fill(g, v);
+      __syncthreads();
+    }
+    g = -1;
+    seg = end;
+    for (; r < end; r += a.teams) {
+      if (a.direct && r / a.group != g) {
+        g = r / a.group;
+        t.sync();  // the row before has been read
+#pragma unroll 1
+        for (int v = t.tid; v <= nvec; v += t.threads) fill(g, v);
+        t.sync();
+      }
+      ring_wait(a.depth);
+      __syncwarp();  // what the other lanes have copied
+      const char* at = ring + at_stage;
+      f2 f[kV][4];
+      float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
+      if (kBranch) {
+        f2 m = 0, s = both(1.f);
+        if (a.post != BASA_NORM_NONE) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
+          for (int j = 0; j < kV; ++j) Part<TY, kV>::take(at + x_bytes, j, t, f[j]);
+          post = row_stats<kV>(f, c.ok, a.post, a.post_eps, a.inv, n, inv_n, t);
+          m = both(-post.x);
+          s = both(post.y);
+        }
+        const f2 res = both(a.res);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          f2 u[4], G[4];
+          Part<TY, kV>::take(at + x_bytes, j, t, u);
+          Part<TX, kV>::take(at, j, t, f[j]);
+          get8(sG + c.at[j], half, G);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            f[j][i] = fma2(mul2(add2(f[j][i], m), s), S[j][i], B[j][i]);
-          store8(h + j * next, f[j]);
+            f[j][i] = fma2(mul2(add2(u[i], m), s), G[i], mul2(res, f[j][i]));
+          if (c.ok[j]) put_row(xo + c.col[j], f[j], a.wide);
         }
-      h += a.C;
+        xo += skip;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) Part<TX, kV>::take(at, j, t, f[j]);
+      }
+      fetch(at_stage);  // the row's elements are in registers, their stage is free
+      at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
+      if (kNorm) {
+        pre = row_stats<kV>(f, c.ok, a.norm, a.eps, a.inv, n, inv_n, t);
+        const f2 m = both(-pre.x), s = both(pre.y);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          f2 S[4], B[4];
+          get8(sS + c.at[j], half, S);
+          get8(sB + c.at[j], half, B);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[j][i] = fma2(mul2(add2(f[j][i], m), s), S[i], B[i]);
+          if (c.ok[j]) put_row(h + c.col[j], f[j], a.wide);
+        }
+        h += skip;
+      }
+      if (a.stats && t.tid == 0) a.stats[r] = make_float4(pre.x, pre.y, post.x, post.y);
     }
-    if (a.stats && tid == 0) a.stats[r] = make_float4(pre.x, pre.y, post.x, post.y);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward
+// Backward.  A CTA is one team and takes a contiguous range of rows, kR at a
+// time; a thread's columns of the three sums over rows stay in registers.  Rows
+// at a time share the factors read, the waits, the barriers and the addresses,
+// and their chains of exchanges run side by side; of one modulation row's
+// rows an odd last one has a row of zeros beside it.
 // ---------------------------------------------------------------------------
 template <int kV>
 struct ColSums {
@@ -291,8 +475,8 @@ struct ColSums {
 // this CTA's range, into the CTA's partial rows otherwise; and, times the
 // modulation, into the CTA's partial rows of the weights.
 template <int kV, bool kBranch, bool kNorm>
-__device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, long long g, bool whole,
-                                   bool first, bool again) {
+__device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, long long g,
+                                      bool whole, bool first, bool again) {
   float* pg = a.part_g + ((long long)blockIdx.x * 2 + (first ? 0 : 1)) * 3 * a.C;
   float* pw = a.part_w + (long long)blockIdx.x * 3 * a.C;
 #pragma unroll
@@ -351,55 +535,89 @@ __device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, lon
   }
 }
 
-template <typename TX, typename TY, int kV, int kThreads, bool kBranch, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 1) gnorm_bwd_kernel(const __grid_constant__ GnArgs a) {
-  extern __shared__ __align__(16) char ring[];
-  __shared__ RowSmem sm;
-  const int tid = threadIdx.x, threads = blockDim.x, nvec = a.C / 8;
-  bool ok[kV];
-#pragma unroll
-  for (int j = 0; j < kV; ++j) ok[j] = j * threads + tid < nvec;
-  const int next = threads * 8;
-  const int xb = Slot<TX>::bytes(kV, threads), yb = Slot<TY>::bytes(kV, threads);
+template <typename TX, typename TY, int kV, int kR, int kThreads, bool kBranch, bool kNorm>
+__global__ void __launch_bounds__(kThreads, 1)
+    gnorm_bwd_kernel(const __grid_constant__ GnArgs a) {
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ float4 red[2][kMaxWarps];
+  const int nvec = a.C / 8;
+  Team t;
+  t.warps = blockDim.x >> 5;
+  t.lane = threadIdx.x & 31;
+  t.id = 0;
+  t.warp = threadIdx.x >> 5;
+  t.threads = blockDim.x;
+  t.tid = threadIdx.x;
+  t.red = red;
+  t.buf = 0;
+  Cols<kV> c;
+  c.init(t, nvec);
+  Part<TX, kV> lx;
+  Part<TY, kV> ly;
+  lx.init(t, nvec);
+  ly.init(t, nvec);
+  const int xb = Part<TX, kV>::bytes(t.threads), yb = Part<TY, kV>::bytes(t.threads);
   const int o_y = a.gx ? xb : 0, o_x = o_y + (a.need_y ? yb : 0), o_gh = o_x + xb;
-  const int stage = kNorm ? o_gh + yb : o_x;
+  const int row_bytes = kNorm ? o_gh + yb : o_x, stage = kR * row_bytes;
+  const int half = factor_half(nvec);
+  char* const sG = dyn;
+  char* const sS = sG + (kBranch ? 2 * half : 0);
+  char* const ring = sS + (kNorm ? 2 * half : 0);
+  const uint32_t ring_at = shared_u32(ring);
   const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
   const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
-  long long from = (long long)r0 * a.C + tid * 8, to = from;  // of the next row read, written
-  const uint32_t ring_at = shared_u32(ring);
-  int ahead = 0, to_stage = 0;
-  auto fetch = [&]() {
-    if (r0 + ahead < r1) {
-      const uint32_t at = ring_at + to_stage;
+  const long long off = (long long)r0 * a.C;
+  const TX* px = kNorm ? static_cast<const TX*>(a.x) + off : nullptr;
+  const TY* pgh = kNorm ? static_cast<const TY*>(a.gh) + off : nullptr;
+  const TX* pgx = a.gx ? static_cast<const TX*>(a.gx) + off : nullptr;
+  const TY* py = a.need_y ? static_cast<const TY*>(a.y) + off : nullptr;
+  TX* dx = static_cast<TX*>(a.dx) + off;
+  TY* dy = kBranch ? static_cast<TY*>(a.dy) + off : nullptr;
+  long long g = r0 / a.group;
+  int ahead = r0, ahead_end = (int)min((long long)r1, (g + 1) * a.group), at_stage = 0;
+  auto fetch = [&](int to) {
+    __syncwarp();  // every lane has read what the stage held
+    if (ahead < r1) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
-          const long long e = from + j * next;
-          if (kNorm) {
-            Slot<TX>::fetch(at + o_x, static_cast<const TX*>(a.x) + e, j, threads, tid);
-            Slot<TY>::fetch(at + o_gh, static_cast<const TY*>(a.gh) + e, j, threads, tid);
-          }
-          if (a.gx) Slot<TX>::fetch(at, static_cast<const TX*>(a.gx) + e, j, threads, tid);
-          if (kBranch && a.need_y)
-            Slot<TY>::fetch(at + o_y, static_cast<const TY*>(a.y) + e, j, threads, tid);
+      for (int k = 0; k < kR; ++k) {
+        const uint32_t at = ring_at + to + k * row_bytes;
+        const bool on = k == 0 || ahead < ahead_end;
+        if (kNorm) {
+          lx.fetch(at + o_x, px, on);
+          ly.fetch(at + o_gh, pgh, on);
         }
-      from += a.C;
+        if (a.gx) lx.fetch(at, pgx, on);
+        if (kBranch && a.need_y) ly.fetch(at + o_y, py, on);
+        if (on) {
+          if (kNorm) {
+            px += a.C;
+            pgh += a.C;
+          }
+          if (a.gx) pgx += a.C;
+          if (kBranch && a.need_y) py += a.C;
+          ++ahead;
+        }
+      }
+      if (ahead == ahead_end) ahead_end = (int)min((long long)r1, ahead + a.group);
     }
     copy_commit();
-    ++ahead;
-    to_stage = to_stage + stage == a.depth * stage ? 0 : to_stage + stage;
   };
-  for (int s = 0; s < a.depth - 1; ++s) fetch();
-  f2 G[kV][4], S[kV][4];  // gate * pw, (1 + scale) * w
+  for (int s = 0; s < a.depth; ++s) fetch(s * stage);
   ColSums<kV> sum;
-  long long g = r0 / a.group, g_end = r0;
+  int end = r0;
   const long long g_first = g;
   bool flushed = false;
-  int buf = 0, at_stage = 0;
-  float4 st = make_float4(0.f, 0.f, 0.f, 0.f), st_next = st;
-  if (a.st) st_next = __ldg(a.st + r0);
-  for (int r = r0;; ++r) {
-    if (r >= g_end || r == r1) {
+  float4 st_next[kR];
+  auto stats_of = [&](int r) {  // of the rows from r on, ahead of their use
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      st_next[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.st && r + k < r1) st_next[k] = __ldg(a.st + r + k);
+    }
+  };
+  stats_of(r0);
+  for (int r = r0;;) {
+    if (r == end) {
       if (r > r0) {
         flush<kV, kBranch, kNorm>(a, sum, g, g * a.group >= r0 && (g + 1) * a.group <= r,
                                   g == g_first, flushed);
@@ -407,122 +625,140 @@ __global__ void __launch_bounds__(kThreads, 1) gnorm_bwd_kernel(const __grid_con
       }
       if (r == r1) break;
       g = r / a.group;
-      g_end = (g + 1) * a.group;
+      end = (int)min((long long)r1, (g + 1) * a.group);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        const long long c = ok[j] ? tid * 8 + j * next : 0;
-        f2 p[4];
+      for (int j = 0; j < kV; ++j) {  // each thread reads the factors that it writes
+        f2 p[4] = {0, 0, 0, 0}, q[4];
         if (kBranch) {
-          param8(a.gate, a.mod_bf16, g * a.ld_gate + c, 1.f, G[j]);
-          param8(a.pw, a.w_bf16, c, 1.f, p);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) G[j][i] = mul2(G[j][i], p[i]);
+          if (c.ok[j]) gate8(a, g, c.col[j], p);
+          put8(sG + c.at[j], half, p);
         }
         if (kNorm) {
-          param8(a.scale, a.mod_bf16, g * a.ld_scale + c, 0.f, p);
-          param8(a.w, a.w_bf16, c, 1.f, S[j]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) S[j][i] = mul2(S[j][i], add2(p[i], both(1.f)));
+          if (c.ok[j]) scale8(a, g, c.col[j], p, q);
+          put8(sS + c.at[j], half, p);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum.a[j][i] = sum.s[j][i] = sum.d[j][i] = 0;
       }
     }
-    fetch();
-    st = st_next;
-    if (a.st && r + 1 < r1) st_next = __ldg(a.st + r + 1);
-    ring_wait(a.depth);
-    const char* at = ring + at_stage;
-    at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
-    f2 t[kV][4];
-    if (kNorm) {
-      const f2 m = both(-st.x), s = both(st.y);
-      f2 xh[kV][4], s1 = 0, s2 = 0;
+    float4 st[kR];
+    bool on[kR];
+    int rows = 0;
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
-          take<TX>(at + o_x, j, xh[j]);
-          take<TY>(at + o_gh, j, t[j]);
+    for (int k = 0; k < kR; ++k) {
+      on[k] = r + k < end;
+      rows += on[k] ? 1 : 0;
+      st[k] = st_next[k];
+    }
+    stats_of(r + rows);
+    ring_wait(a.depth);
+    __syncwarp();  // what the other lanes have copied
+    const char* at = ring + at_stage;
+    f2 xh[kR][kV][4], v[kR][kV][4];  // xh; a, then t, then e
+    float2 c12[kR];
+    if (kNorm) {
+      float2 part[kR];
+      f2 s1[kR], s2[kR];
+#pragma unroll
+      for (int k = 0; k < kR; ++k) s1[k] = s2[k] = 0;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        f2 S[4];
+        get8(sS + c.at[j], half, S);
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+          const f2 m = both(-st[k].x), s = both(st[k].y);
+          Part<TX, kV>::take(at + k * row_bytes + o_x, j, t, xh[k][j]);
+          Part<TY, kV>::take(at + k * row_bytes + o_gh, j, t, v[k][j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            xh[j][i] = mul2(add2(xh[j][i], m), s);
-            sum.a[j][i] = fma2(t[j][i], xh[j][i], sum.a[j][i]);
-            sum.s[j][i] = add2(sum.s[j][i], t[j][i]);
-            t[j][i] = mul2(t[j][i], S[j][i]);
-            s1 = add2(s1, t[j][i]);
-            s2 = fma2(t[j][i], xh[j][i], s2);
+            xh[k][j][i] = mul2(add2(xh[k][j][i], m), s);
+            sum.a[j][i] = fma2(v[k][j][i], xh[k][j][i], sum.a[j][i]);
+            sum.s[j][i] = add2(sum.s[j][i], v[k][j][i]);
+            v[k][j][i] = mul2(v[k][j][i], S[i]);
+            s1[k] = add2(s1[k], v[k][j][i]);
+            s2[k] = fma2(v[k][j][i], xh[k][j][i], s2[k]);
           }
         }
-      const float2 v = row_sum2(s1, s2, sm, buf);
-      // t = rstd (a - mean(a) - xh mean(a xh)) + gx
-      const f2 c1 = both(a.norm == BASA_NORM_LAYER ? -v.x * a.inv : 0.f), c2 = both(-v.y * a.inv);
+      }
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) {
-          f2 gx[4] = {0, 0, 0, 0};
-          if (a.gx) take<TX>(at, j, gx);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            t[j][i] = fma2(s, add2(fma2(xh[j][i], c2, t[j][i]), c1), gx[i]);
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) take<TX>(at, j, t[j]);
+      for (int k = 0; k < kR; ++k) part[k] = make_float2(sum2(s1[k]), sum2(s2[k]));
+      t.sums(part, c12);
     }
+    f2 s1[kR], s2[kR];
+#pragma unroll
+    for (int k = 0; k < kR; ++k) s1[k] = s2[k] = 0;
     const f2 res = both(a.res);
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
-      if (ok[j]) {
-        f2 v[4];
+    for (int j = 0; j < kV; ++j) {
+      f2 G[4];
+      if (kBranch) get8(sG + c.at[j], half, G);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mul2(res, t[j][i]);
-        store8(static_cast<TX*>(a.dx) + to + j * next, v);
-      }
-    if (kBranch) {
-      if (a.post == BASA_NORM_NONE) {
+      for (int k = 0; k < kR; ++k) {
+        const char* row = at + k * row_bytes;
+        f2 gx[4] = {0, 0, 0, 0};
+        if (a.gx) Part<TX, kV>::take(row, j, t, gx);
+        if (kNorm) {  // rstd (a - mean(a) - xh mean(a xh)) + gx
+          const f2 s = both(st[k].y);
+          const f2 c1 = both(a.norm == BASA_NORM_LAYER ? -c12[k].x * a.inv : 0.f),
+                   c2 = both(-c12[k].y * a.inv);
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (ok[j]) {
-            if (a.need_y) {
-              f2 y[4];
-              take<TY>(at + o_y, j, y);
+          for (int i = 0; i < 4; ++i)
+            gx[i] = fma2(s, fma2(xh[k][j][i], c2, add2(v[k][j][i], c1)), gx[i]);
+        }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sum.d[j][i] = fma2(t[j][i], y[i], sum.d[j][i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) t[j][i] = mul2(t[j][i], G[j][i]);
-          }
-      } else {
-        const f2 m = both(-st.z), s = both(st.w);
-        f2 yh[kV][4], s1 = 0, s2 = 0;
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (ok[j]) {
-            take<TY>(at + o_y, j, yh[j]);
+        for (int i = 0; i < 4; ++i) v[k][j][i] = mul2(res, gx[i]);
+        if (c.ok[j] && on[k]) put_row(dx + k * a.C + c.col[j], v[k][j], a.wide);
+        if (kBranch) {
+          f2 yh[4] = {0, 0, 0, 0};
+          if (a.need_y) Part<TY, kV>::take(row + o_y, j, t, yh);
+          if (a.post == BASA_NORM_NONE) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              yh[j][i] = mul2(add2(yh[j][i], m), s);
-              sum.d[j][i] = fma2(t[j][i], yh[j][i], sum.d[j][i]);
-              t[j][i] = mul2(t[j][i], G[j][i]);
-              s1 = add2(s1, t[j][i]);
-              s2 = fma2(t[j][i], yh[j][i], s2);
+              sum.d[j][i] = fma2(gx[i], yh[i], sum.d[j][i]);
+              v[k][j][i] = mul2(gx[i], G[i]);
+            }
+            if (c.ok[j] && on[k]) put_row(dy + k * a.C + c.col[j], v[k][j], a.wide);
+          } else {
+            const f2 pm = both(-st[k].z), ps = both(st[k].w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              yh[i] = mul2(add2(yh[i], pm), ps);
+              sum.d[j][i] = fma2(gx[i], yh[i], sum.d[j][i]);
+              v[k][j][i] = mul2(gx[i], G[i]);
+              s1[k] = add2(s1[k], v[k][j][i]);
+              s2[k] = fma2(v[k][j][i], yh[i], s2[k]);
             }
           }
-        const float2 v = row_sum2(s1, s2, sm, buf);
-        const f2 c1 = both(a.post == BASA_NORM_LAYER ? -v.x * a.inv : 0.f), c2 = both(-v.y * a.inv);
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (ok[j])
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              t[j][i] = mul2(s, add2(fma2(yh[j][i], c2, t[j][i]), c1));
+        }
       }
-#pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (ok[j]) store8(static_cast<TY*>(a.dy) + to + j * next, t[j]);
     }
-    to += a.C;
+    if (kBranch && a.post != BASA_NORM_NONE) {
+      float2 part[kR];
+#pragma unroll
+      for (int k = 0; k < kR; ++k) part[k] = make_float2(sum2(s1[k]), sum2(s2[k]));
+      t.sums(part, c12);
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        const f2 pm = both(-st[k].z), ps = both(st[k].w);
+        const f2 c1 = both(a.post == BASA_NORM_LAYER ? -c12[k].x * a.inv : 0.f),
+                 c2 = both(-c12[k].y * a.inv);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          f2 yh[4];
+          Part<TY, kV>::take(at + k * row_bytes + o_y, j, t, yh);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[k][j][i] = mul2(ps, fma2(mul2(add2(yh[i], pm), ps), c2, add2(v[k][j][i], c1)));
+          if (c.ok[j] && on[k]) put_row(dy + k * a.C + c.col[j], v[k][j], a.wide);
+        }
+      }
+    }
+    fetch(at_stage);
+    at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
+    dx += rows * a.C;
+    if (kBranch) dy += rows * a.C;
+    r += rows;
   }
 }
 
@@ -603,6 +839,7 @@ __global__ void __launch_bounds__(256) gnorm_join_kernel(GnJoin a) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 int round32(int x) { return (x + 31) / 32 * 32; }
 
 basa_status check_gnorm(const basa_gnorm_params* p) {
@@ -646,7 +883,7 @@ GnArgs gnorm_args(const basa_gnorm_params* p) {
   return a;
 }
 
-constexpr int kSmemCta = 220 * 1024;  // of the 227 KB a CTA may have; the rest is static
+constexpr int kSmem = 224 * 1024;  // of an SM's 228 KB, beside static parts and the CTAs' own 1 KB
 
 template <typename K>
 basa_status go(K kernel, const GnArgs& a, unsigned grid, int threads, int smem, cudaStream_t st) {
@@ -657,47 +894,65 @@ basa_status go(K kernel, const GnArgs& a, unsigned grid, int threads, int smem, 
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }
 
-template <typename TX, typename TY, int kThreads, int kCtas>
-basa_status go_fwd_t(GnArgs a, int threads, cudaStream_t st) {
+template <typename TX, typename TY, int kV>
+basa_status go_fwd_v(GnArgs a, cudaStream_t st) {
   const bool branch = a.y != nullptr, norm = a.norm != BASA_NORM_NONE;
-  const int stage = Slot<TX>::bytes(2, threads) + (branch ? Slot<TY>::bytes(2, threads) : 0);
-  a.depth = 3;
-  const int smem = a.depth * stage;
-  int per_sm = kSmemCta / (smem + 1024);
-  const int by_regs = kThreads * kCtas / threads;
-  if (per_sm > by_regs) per_sm = by_regs;
-  if (per_sm < 1) per_sm = 1;
-  const long long cap = (long long)row_sm_count() * per_sm;
-  const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
-  if (branch && norm)
-    return go(gnorm_kernel<TX, TY, 2, kThreads, kCtas, true, true>, a, grid, threads, smem, st);
-  if (branch)
-    return go(gnorm_kernel<TX, TY, 2, kThreads, kCtas, true, false>, a, grid, threads, smem, st);
-  return go(gnorm_kernel<TX, TY, 2, kThreads, kCtas, false, true>, a, grid, threads, smem, st);
+  const int per_row = 32 * a.warps;
+  const int stage = Part<TX, kV>::bytes(per_row) + (branch ? Part<TY, kV>::bytes(per_row) : 0);
+  const int sms = row_sm_count();
+  const unsigned grid = (unsigned)(a.rows < sms ? a.rows : sms);
+  const long long most = (a.rows + grid - 1) / grid;  // rows of a CTA
+  const int factors = ((branch ? 1 : 0) + (norm ? 2 : 0)) * 2 * factor_half(a.C / 8);
+  a.teams = kFwdThreads / per_row;
+  if (a.warps > 1 && a.teams > 15) a.teams = 15;  // barriers of a CTA
+  if (a.teams > most) a.teams = (int)most;
+  a.direct = a.group < 4 * a.teams;
+  // shared memory: the factors, once or for each team, and a ring for each team
+  const int fit = a.direct ? kSmem / (factors + stage) : (kSmem - factors) / stage;
+  if (a.teams > fit) a.teams = fit;
+  const int held = a.direct ? a.teams * factors : factors;
+  a.depth = (kSmem - held) / (a.teams * stage);
+  if (a.depth > 3) a.depth = 3;
+  const int smem = held + a.teams * a.depth * stage, threads = a.teams * per_row;
+  if (branch && norm) return go(gnorm_kernel<TX, TY, kV, true, true>, a, grid, threads, smem, st);
+  if (branch) return go(gnorm_kernel<TX, TY, kV, true, false>, a, grid, threads, smem, st);
+  return go(gnorm_kernel<TX, TY, kV, false, true>, a, grid, threads, smem, st);
 }
 template <typename TX, typename TY>
-basa_status go_fwd(const GnArgs& a, cudaStream_t st) {
-  const int threads = round32((a.C / 8 + 1) / 2);
-  if (threads <= 128) return go_fwd_t<TX, TY, 128, 4>(a, threads, st);
-  if (threads <= 320) return go_fwd_t<TX, TY, 320, 2>(a, threads, st);
-  return go_fwd_t<TX, TY, 512, 1>(a, threads, st);
+basa_status go_fwd(GnArgs a, cudaStream_t st) {
+  const int nvec = a.C / 8;
+  a.warps = (nvec + 127) / 128;
+  const int v = (nvec + 32 * a.warps - 1) / (32 * a.warps);
+  return v == 4   ? go_fwd_v<TX, TY, 4>(a, st)
+         : v == 3 ? go_fwd_v<TX, TY, 3>(a, st)
+         : v == 2 ? go_fwd_v<TX, TY, 2>(a, st)
+                  : go_fwd_v<TX, TY, 1>(a, st);
 }
 
-// Launch shape of the backward: vectors a thread and CTAs.  Sums in registers
-// cost 40 fp32 a vector, so a thread takes one vector up to 640 threads (102
-// registers each), two beyond.
+// Launch shape of the backward.  Two vectors a thread (their sums: 48 registers)
+// and two rows at a time up to 320 threads (168 registers each); beyond, rows of
+// more than 5120 columns, one row at a time.
 struct BwdShape {
-  int v, threads;
+  int threads, rows, per_sm, bytes;  // bytes: shared memory beside the ring; rows at a time
   long long grid;
 };
+constexpr int kBwdV = 2, kBwdThreads = 320;
+int bwd_row_bytes(const basa_gnorm_params* p, int threads) {
+  const int sx = p->x_dtype == BASA_BF16 ? 2 : 4, sy = p->dtype == BASA_BF16 ? 2 : 4;
+  return kBwdV * threads * 8 * 2 * (sx + sy);
+}
 BwdShape bwd_shape(const basa_gnorm_params* p) {
   BwdShape s;
   const int nvec = p->C / 8;
-  s.v = nvec <= 640 ? 1 : 2;
-  s.threads = round32((nvec + s.v - 1) / s.v);
-  int per_sm = (s.v == 1 ? 640 : 512) / s.threads;
-  if (per_sm > 8) per_sm = 8;
-  long long cap = (long long)row_sm_count() * per_sm;
+  s.threads = round32((nvec + kBwdV - 1) / kBwdV);
+  s.rows = s.threads <= kBwdThreads ? 2 : 1;
+  s.bytes = 4 * factor_half(nvec);
+  const int need = s.bytes + s.rows * bwd_row_bytes(p, s.threads) + 2048;
+  s.per_sm = (s.threads <= kBwdThreads ? kBwdThreads : 512) / s.threads;
+  if (s.per_sm > kSmem / need) s.per_sm = kSmem / need;
+  if (s.per_sm > 8) s.per_sm = 8;
+  if (s.per_sm < 1) s.per_sm = 1;
+  long long cap = (long long)row_sm_count() * s.per_sm;
   const long long few = (p->rows + 3) / 4;  // at least four rows a CTA
   if (cap > few) cap = few;
   s.grid = cap < 1 ? 1 : cap;
@@ -710,26 +965,28 @@ size_t part_w_bytes(const basa_gnorm_params* p, const BwdShape& s) {
   return up256((size_t)s.grid * 3 * p->C * sizeof(float));
 }
 
-template <typename TX, typename TY, int kV, int kThreads>
-basa_status go_bwd_v(GnArgs a, const BwdShape& s, cudaStream_t st) {
+template <typename TX, typename TY, int kR, int kThreads>
+basa_status go_bwd_t(GnArgs a, const BwdShape& s, cudaStream_t st) {
   const bool branch = a.dy != nullptr, norm = a.norm != BASA_NORM_NONE;
-  const int xb = Slot<TX>::bytes(kV, s.threads), yb = Slot<TY>::bytes(kV, s.threads);
-  const int stage = (a.gx ? xb : 0) + (a.need_y ? yb : 0) + (norm ? xb + yb : 0);
-  const int ctas = (kV == 1 ? 640 : 512) / s.threads;
-  const int room = kSmemCta / (ctas < 1 ? 1 : ctas > 8 ? 8 : ctas) - 1024;
-  a.depth = room / stage;
+  const int xb = Part<TX, kBwdV>::bytes(s.threads), yb = Part<TY, kBwdV>::bytes(s.threads);
+  const int stage = kR * ((a.gx ? xb : 0) + (a.need_y ? yb : 0) + (norm ? xb + yb : 0));
+  a.depth = (kSmem / s.per_sm - 2048 - s.bytes) / stage;
   a.depth = a.depth > 3 ? 3 : a.depth < 1 ? 1 : a.depth;
-  const int smem = a.depth * stage;
+  const int smem = s.bytes + a.depth * stage;
   const unsigned grid = (unsigned)s.grid;
   if (branch && norm)
-    return go(gnorm_bwd_kernel<TX, TY, kV, kThreads, true, true>, a, grid, s.threads, smem, st);
+    return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, true, true>, a, grid, s.threads, smem,
+              st);
   if (branch)
-    return go(gnorm_bwd_kernel<TX, TY, kV, kThreads, true, false>, a, grid, s.threads, smem, st);
-  return go(gnorm_bwd_kernel<TX, TY, kV, kThreads, false, true>, a, grid, s.threads, smem, st);
+    return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, true, false>, a, grid, s.threads, smem,
+              st);
+  return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, false, true>, a, grid, s.threads, smem,
+            st);
 }
 template <typename TX, typename TY>
 basa_status go_bwd(const GnArgs& a, const BwdShape& s, cudaStream_t st) {
-  return s.v == 1 ? go_bwd_v<TX, TY, 1, 640>(a, s, st) : go_bwd_v<TX, TY, 2, 512>(a, s, st);
+  return s.rows == 2 ? go_bwd_t<TX, TY, 2, kBwdThreads>(a, s, st)
+                     : go_bwd_t<TX, TY, 1, 512>(a, s, st);
 }
 
 }  // namespace
@@ -760,6 +1017,7 @@ basa_status basa_gated_norm(const void* x, const void* y, const void* gate, cons
   a.w = weight; a.b = bias; a.scale = scale; a.shift = shift;
   a.xo = x_out; a.h = h;
   a.stats = reinterpret_cast<float4*>(stats);
+  a.wide = aligned32(x_out) && aligned32(h);
   if (p->x_dtype == BASA_BF16) return go_fwd<__nv_bfloat16, __nv_bfloat16>(a, stream);
   if (p->dtype == BASA_BF16) return go_fwd<float, __nv_bfloat16>(a, stream);
   return go_fwd<float, float>(a, stream);
@@ -822,6 +1080,7 @@ basa_status basa_gated_norm_bwd(const void* dh, const void* x_out, const float* 
   a.dx = dx; a.dy = dy;
   a.dgate = dgate; a.dscale = dscale; a.dshift = dshift;
   a.need_y = need_y;
+  a.wide = aligned32(dx) && aligned32(dy);
   char* ws = static_cast<char*>(workspace);
   if (mods) a.part_g = reinterpret_cast<float*>(ws);
   if (weights) a.part_w = reinterpret_cast<float*>(ws + part_g_bytes(p, sh));
