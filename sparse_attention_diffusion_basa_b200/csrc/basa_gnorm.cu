@@ -80,107 +80,54 @@ struct Team {
     else
       asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
   }
-  __device__ __forceinline__ const float4* share(float4 v) {
-    float4* at = reinterpret_cast<float4*>(red[buf]);
+  __device__ __forceinline__ float* next() {
+    float* at = reinterpret_cast<float*>(red[buf]);
     buf ^= 1;
-    if (lane == 0) at[warp] = v;
-    sync();
     return at;
   }
-  // Two sums of one row, or of each of two rows.
+  // Two sums of one row, or of each of two rows.  Lanes that hold a sum's halves
+  // of the warp keep one sum and hand on the others (six exchanges for four
+  // sums); every warp then adds up the warps' parts, one a lane.
   __device__ __forceinline__ void sums(const float2 (&v)[1], float2 (&s)[1]) {
-    const float2 w = lane_sum<32>(v[0]);
-    const float4* p = share(make_float4(w.x, w.y, 0.f, 0.f));
-    s[0] = make_float2(0.f, 0.f);
-    for (int i = 0; i < warps; ++i) {
-      const float2 u = *reinterpret_cast<const float2*>(p + i);
-      s[0].x += u.x;
-      s[0].y += u.y;
-    }
+    const bool hi = lane & 16;
+    float k = (hi ? v[0].y : v[0].x) + __shfl_xor_sync(0xffffffffu, hi ? v[0].x : v[0].y, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    float* at = next();
+    if ((lane & 15) == 0) at[2 * warp + (lane >> 4)] = k;
+    sync();
+    k = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 32 * i < 2 * warps) k += at[lane + 32 * i];
+#pragma unroll
+    for (int o = 16; o > 1; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    s[0].x = __shfl_sync(0xffffffffu, k, 0);
+    s[0].y = __shfl_sync(0xffffffffu, k, 1);
   }
   __device__ __forceinline__ void sums(const float2 (&v)[2], float2 (&s)[2]) {
-    float4 w = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    const bool hi = lane & 16, mid = lane & 8;
+    const float a = (hi ? v[1].x : v[0].x) + __shfl_xor_sync(0xffffffffu, hi ? v[0].x : v[1].x, 16);
+    const float b = (hi ? v[1].y : v[0].y) + __shfl_xor_sync(0xffffffffu, hi ? v[0].y : v[1].y, 16);
+    float k = (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w.x += __shfl_xor_sync(0xffffffffu, w.x, o);
-      w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
-      w.z += __shfl_xor_sync(0xffffffffu, w.z, o);
-      w.w += __shfl_xor_sync(0xffffffffu, w.w, o);
-    }
-    const float4* p = share(w);
-    s[0] = s[1] = make_float2(0.f, 0.f);
-    for (int i = 0; i < warps; ++i) {
-      const float4 u = p[i];
-      s[0].x += u.x;
-      s[0].y += u.y;
-      s[1].x += u.z;
-      s[1].y += u.w;
-    }
+    for (int o = 4; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    float* at = next();
+    if ((lane & 7) == 0) at[4 * warp + (lane >> 3)] = k;
+    sync();
+    k = 0.f;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (lane + 32 * i < 4 * warps) k += at[lane + 32 * i];
+#pragma unroll
+    for (int o = 16; o > 2; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+    s[0].x = __shfl_sync(0xffffffffu, k, 0);
+    s[0].y = __shfl_sync(0xffffffffu, k, 1);
+    s[1].x = __shfl_sync(0xffffffffu, k, 2);
+    s[1].y = __shfl_sync(0xffffffffu, k, 3);
   }
 };
-
-// Elements of a row in this warp.
-__device__ __forceinline__ float elements_of(const Team& t, int kv, int nvec) {
-  int n = 0;
-  for (int j = 0; j < kv; ++j) {
-    const int left = nvec - j * t.threads - 32 * t.warp;
-    n += left < 0 ? 0 : left > 32 ? 32 : left;
-  }
-  return (float)(8 * n);
-}
-
-// (mean, rstd) of a row held kV * 8 values a thread, zeros where ok is false.
-// Layer: the squares are taken about each warp's own mean and joined about the
-// row's (Chan, Golub and LeVeque's update), so a mean far from zero costs no
-// digits and one barrier is enough.  n, inv_n: elements of the warp.
-template <int kV>
-__device__ __forceinline__ float2 row_stats(const f2 (&f)[kV][4], const bool (&ok)[kV], int kind,
-                                            float eps, float inv, float n, float inv_n, Team& t) {
-  f2 q0 = 0, q1 = 0;
-  if (kind == BASA_NORM_LAYER) {
-    f2 s0 = 0, s1 = 0;
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        s0 = add2(s0, f[j][i]);
-        s1 = add2(s1, f[j][i + 1]);
-      }
-    const float m = lane_sum<32>(sum2(add2(s0, s1))) * inv_n;
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const f2 mm = both(ok[j] ? -m : 0.f);
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const f2 a = add2(f[j][i], mm), b = add2(f[j][i + 1], mm);
-        q0 = fma2(a, a, q0);
-        q1 = fma2(b, b, q1);
-      }
-    }
-    const float q = lane_sum<32>(sum2(add2(q0, q1)));
-    const float4* p = t.share(make_float4(m, q, n, 0.f));
-    float mean = 0.f, m2 = 0.f;
-    for (int i = 0; i < t.warps; ++i) mean = fmaf(p[i].x, p[i].z, mean);
-    mean *= inv;
-    for (int i = 0; i < t.warps; ++i) {
-      const float4 w = p[i];
-      const float d = w.x - mean;
-      m2 += fmaf(w.z * d, d, w.y);
-    }
-    return make_float2(mean, rsqrtf(m2 * inv + eps));
-  }
-#pragma unroll
-  for (int j = 0; j < kV; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      q0 = fma2(f[j][i], f[j][i], q0);
-      q1 = fma2(f[j][i + 1], f[j][i + 1], q1);
-    }
-  const float4* p = t.share(make_float4(lane_sum<32>(sum2(add2(q0, q1))), 0.f, 0.f, 0.f));
-  float q = 0.f;
-  for (int i = 0; i < t.warps; ++i) q += p[i].x;
-  return make_float2(0.f, rsqrtf(q * inv + eps));
-}
+static_assert(kMaxWarps <= 24, "Team::sums reads three parts a lane");
 
 // A modulation row's factors for the eight columns from `col`: gate * pw of the
 // branch; (1 + scale) * w and (1 + scale) * b + shift of the norm.
@@ -221,6 +168,9 @@ __device__ __forceinline__ void affine8(const GnArgs& a, long long g, int col, f
 // first pieces of all vectors and then the second ones, `half` bytes further.
 // One more vector of zeros stands for all vectors past the row's end.
 __host__ __device__ constexpr int factor_half(int nvec) { return (nvec + 1) * 16; }
+// Stages begin at 128 bytes: a request of an asynchronous copy whose destination
+// does not is split (measured: 1.5 times as many at the L2).
+__host__ __device__ constexpr int up128(int x) { return (x + 127) & ~127; }
 __device__ __forceinline__ void put8(char* at, int half, const f2 (&f)[4]) {
   *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f[0], f[1]);
   *reinterpret_cast<ulonglong2*>(at + half) = make_ulonglong2(f[2], f[3]);
@@ -233,67 +183,49 @@ __device__ __forceinline__ void get8(const char* at, int half, f2 (&f)[4]) {
   f[2] = y.x;
   f[3] = y.y;
 }
-// A thread's columns of a row: vector j of eight at col[j], whether it is inside
+// A thread's columns of a row: vector j of eight at col(j), whether it is inside
 // the row, and where its factors lie.  Vectors past the row's end are filled
 // with zeros on the way in, have factors of zero, are computed with like the
 // others (to zeros) and not stored, so the loops over a thread's vectors have no
-// branches.
-template <int kV>
+// branches.  All of it is formed anew where it is used, from few registers: a
+// spilled register costs far more than an addition in kernels whose shared
+// memory leaves almost no L1.
 struct Cols {
-  int col[kV], at[kV];
-  bool ok[kV];
-  __device__ __forceinline__ void init(const Team& t, int nvec) {
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int v = j * t.threads + t.tid;
-      ok[j] = v < nvec;
-      col[j] = ok[j] ? v * 8 : 0;
-      at[j] = (ok[j] ? v : nvec) * 16;
-    }
-  }
+  int first, next, C;  // column of vector 0, from vector to vector, columns of a row
+  __device__ __forceinline__ Cols(const Team& t, int C_)
+      : first(t.tid * 8), next(t.threads * 8), C(C_) {}
+  __device__ __forceinline__ int col(int j) const { return first + j * next; }
+  __device__ __forceinline__ bool ok(int j) const { return col(j) < C; }
+  __device__ __forceinline__ int at(int j) const { return min(col(j), C) * 2; }
 };
 
-// One tensor's part of a ring stage: for each vector of a thread and each warp,
-// the warp's 512 bytes (fp32: 1 KB) as they lie in memory.  bf16: a lane copies
-// its own vector.  fp32: a vector is two 16-byte pieces; the lanes copy
-// consecutive pieces, not their own, so that a request covers whole lines (with
-// a lane's own pieces, 32 bytes apart, the L2 sees one request for each piece).
+// One tensor's part of a ring stage: a row's bytes as they lie in memory, up to
+// the team's vectors.  bf16: a lane copies its own vectors.  fp32: a vector is
+// two 16-byte pieces; the lanes of a warp copy consecutive pieces, not their
+// own, so that a request covers whole lines (with a lane's own pieces, 32 bytes
+// apart, the L2 sees one request for each piece).
 template <typename T, int kV>
 struct Part {
   static constexpr int kPieces = (int)sizeof(T) / 2;
-  int col[kV][kPieces];      // element the lane copies from
-  uint32_t size[kV][kPieces];  // 16, or 0: zeros
-  uint32_t to;               // offset of this warp's first piece of this lane
-  uint32_t step;             // from vector to vector
-  __device__ __forceinline__ void init(const Team& t, int nvec) {
+  int first;  // element of the lane's first piece
+  __device__ __forceinline__ explicit Part(const Team& t)
+      : first(kPieces == 1 ? t.tid * 8 : t.warp * 256 + t.lane * 4) {}
+  static __host__ __device__ constexpr int bytes(int threads) {
+    return kV * threads * kPieces * 16;
+  }
+  __device__ __forceinline__ void fetch(uint32_t at, const T* row, const Cols& c,
+                                        bool on = true) const {
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const int piece = p * 32 + t.lane;  // of the warp's pieces in memory order
-        const int v = j * t.threads + t.warp * 32 + piece / kPieces;
-        col[j][p] = v < nvec ? v * 8 + (piece % kPieces) * 4 : 0;
-        size[j][p] = v < nvec ? 16 : 0;
+        const int e = first + j * c.next + p * 128;
+        const bool in = e < c.C && on;
+        copy16(at + e * (int)sizeof(T), row + (in ? e : 0), in);
       }
-    to = t.warp * kPieces * 512 + t.lane * 16;
-    step = t.warps * kPieces * 512;
   }
-  static __host__ __device__ constexpr int bytes(int threads) {
-    return kV * threads * kPieces * 16;
-  }
-  __device__ __forceinline__ void fetch(uint32_t at, const T* row, bool on = true) const {
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         at + to + j * step + p * 512),
-                     "l"(row + (on ? col[j][p] : 0)), "r"(on ? size[j][p] : 0u)
-                     : "memory");
-  }
-  __device__ __forceinline__ static void take(const char* at, int j, const Team& t, f2 (&f)[4]) {
-    const uint4* s =
-        reinterpret_cast<const uint4*>(at) + ((j * t.warps + t.warp) * 32 + t.lane) * kPieces;
+  __device__ __forceinline__ void take(const char* at, int j, const Cols& c, f2 (&f)[4]) const {
+    const uint4* s = reinterpret_cast<const uint4*>(at + c.col(j) * (int)sizeof(T));
     Raw8<T> r;
     r.a = s[0];
     if constexpr (kPieces == 2) r.b = s[1];
@@ -313,6 +245,88 @@ __device__ __forceinline__ void put_row(float* p, const f2 (&f)[4], bool wide) {
     store8(p, f);
 }
 
+// The same value, but one that the compiler takes for a new one: what is formed
+// from it inside a loop is not moved ahead of the loop, where it would hold
+// registers that the loop does not have.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
+// Keeps the compiler from loading all of a loop's vectors ahead of using the
+// first, for the same reason.
+__device__ __forceinline__ void one_by_one() { asm volatile("" ::: "memory"); }
+
+// Elements of a row in this warp.
+__device__ __forceinline__ float elements_of(const Team& t, int kv, int nvec) {
+  int n = 0;
+  for (int j = 0; j < kv; ++j) {
+    const int left = nvec - j * t.threads - 32 * t.warp;
+    n += left < 0 ? 0 : left > 32 ? 32 : left;
+  }
+  return (float)(8 * n);
+}
+
+// (mean, rstd) of a row held kV * 8 values a thread, zeros past the row's end.
+// Layer: the squares are taken about each warp's own mean and joined about the
+// row's (Chan, Golub and LeVeque's update), so a mean far from zero costs no
+// digits and one barrier is enough.  n, inv_n: elements of the warp.
+template <int kV>
+__device__ __forceinline__ float2 row_stats(const f2 (&f)[kV][4], const Cols& c, int kind,
+                                            float eps, float inv, float n, float inv_n, Team& t) {
+  f2 q0 = 0, q1 = 0;
+  if (kind == BASA_NORM_LAYER) {
+    f2 s0 = 0, s1 = 0;
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        s0 = add2(s0, f[j][i]);
+        s1 = add2(s1, f[j][i + 1]);
+      }
+    const float m = lane_sum<32>(sum2(add2(s0, s1))) * inv_n;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const f2 mm = both(c.ok(j) ? -m : 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const f2 a = add2(f[j][i], mm), b = add2(f[j][i + 1], mm);
+        q0 = fma2(a, a, q0);
+        q1 = fma2(b, b, q1);
+      }
+    }
+    float q = lane_sum<32>(sum2(add2(q0, q1)));
+    float mean = m;
+    if (t.warps > 1) {  // at most eight
+      float4* at = reinterpret_cast<float4*>(t.next());
+      if (t.lane == 0) at[t.warp] = make_float4(m, q, n, 0.f);
+      t.sync();
+      const int i = t.lane & 7;
+      const float4 w = i < t.warps ? at[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      mean = lane_sum<8>(w.x * w.z) * inv;
+      const float d = w.x - mean;
+      q = lane_sum<8>(fmaf(w.z * d, d, w.y));
+    }
+    return make_float2(mean, rsqrtf(q * inv + eps));
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      q0 = fma2(f[j][i], f[j][i], q0);
+      q1 = fma2(f[j][i + 1], f[j][i + 1], q1);
+    }
+  float q = lane_sum<32>(sum2(add2(q0, q1)));
+  if (t.warps > 1) {
+    float* at = t.next();
+    if (t.lane == 0) at[t.warp] = q;
+    t.sync();
+    const int i = t.lane & 7;
+    q = lane_sum<8>(i < t.warps ? at[i] : 0.f);
+  }
+  return make_float2(0.f, rsqrtf(q * inv + eps));
+}
+
 // ---------------------------------------------------------------------------
 // Forward.  One CTA an SM takes a contiguous range of rows, `teams` rows at a
 // time, each in the registers of one team of warps: a row's own sums are a chain
@@ -320,12 +334,12 @@ __device__ __forceinline__ void put_row(float* p, const f2 (&f)[4], bool wide) {
 // row are combined once, in fp32, into shared memory for all the teams (direct:
 // a modulation covers too few rows for that, and each team keeps its own).
 // ---------------------------------------------------------------------------
-constexpr int kFwdThreads = 640;
+constexpr int kFwdThreads = 512;  // 128 registers each
 
 template <typename TX, typename TY, int kV, bool kBranch, bool kNorm>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     gnorm_kernel(const __grid_constant__ GnArgs a) {
-  extern __shared__ __align__(16) char dyn[];
+  extern __shared__ __align__(128) char dyn[];
   __shared__ float4 red[2][kMaxWarps];
   const int nvec = a.C / 8;
   Team t;
@@ -337,15 +351,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   t.tid = 32 * t.warp + t.lane;
   t.red = reinterpret_cast<float4(*)[kMaxWarps]>(&red[0][t.id * t.warps]);
   t.buf = 0;
-  Cols<kV> c;
-  c.init(t, nvec);
-  Part<TX, kV> px;
-  Part<TY, kV> py;
-  px.init(t, nvec);
-  if (kBranch) py.init(t, nvec);
+  Cols c(t, a.C);
+  Part<TX, kV> px(t);
+  Part<TY, kV> py(t);
   const float n = elements_of(t, kV, nvec), inv_n = n > 0.f ? 1.f / n : 0.f;
   const int half = factor_half(nvec), arr = 2 * half;  // bytes of one array of factors
-  const int factors = ((kBranch ? 1 : 0) + (kNorm ? 2 : 0)) * arr;
+  const int factors = up128(((kBranch ? 1 : 0) + (kNorm ? 2 : 0)) * arr);
   char* const sG = dyn + (a.direct ? t.id * factors : 0);
   char* const sS = sG + (kBranch ? arr : 0);
   char* const sB = sS + (kNorm ? arr : 0);
@@ -364,10 +375,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   auto fetch = [&](int to) {
     __syncwarp();  // every lane has read what the stage held
     if (ahead < r1) {
-      px.fetch(ring_at + to, x);
+      px.fetch(ring_at + to, x, c);
       x += skip;
       if (kBranch) {
-        py.fetch(ring_at + to + x_bytes, y);
+        py.fetch(ring_at + to + x_bytes, y, c);
         y += skip;
       }
       ahead += a.teams;
@@ -409,6 +420,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       ring_wait(a.depth);
       __syncwarp();  // what the other lanes have copied
+      c.first = anew(c.first);
+      px.first = anew(px.first);
+      py.first = anew(py.first);
       const char* at = ring + at_stage;
       f2 f[kV][4];
       float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
@@ -416,8 +430,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         f2 m = 0, s = both(1.f);
         if (a.post != BASA_NORM_NONE) {
 #pragma unroll
-          for (int j = 0; j < kV; ++j) Part<TY, kV>::take(at + x_bytes, j, t, f[j]);
-          post = row_stats<kV>(f, c.ok, a.post, a.post_eps, a.inv, n, inv_n, t);
+          for (int j = 0; j < kV; ++j) py.take(at + x_bytes, j, c, f[j]);
+          post = row_stats<kV>(f, c, a.post, a.post_eps, a.inv, n, inv_n, t);
           m = both(-post.x);
           s = both(post.y);
         }
@@ -425,32 +439,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           f2 u[4], G[4];
-          Part<TY, kV>::take(at + x_bytes, j, t, u);
-          Part<TX, kV>::take(at, j, t, f[j]);
-          get8(sG + c.at[j], half, G);
+          py.take(at + x_bytes, j, c, u);
+          px.take(at, j, c, f[j]);
+          get8(sG + c.at(j), half, G);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             f[j][i] = fma2(mul2(add2(u[i], m), s), G[i], mul2(res, f[j][i]));
-          if (c.ok[j]) put_row(xo + c.col[j], f[j], a.wide);
+          if (c.ok(j)) put_row(xo + c.col(j), f[j], a.wide);
+          one_by_one();
         }
         xo += skip;
       } else {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) Part<TX, kV>::take(at, j, t, f[j]);
+        for (int j = 0; j < kV; ++j) px.take(at, j, c, f[j]);
       }
       fetch(at_stage);  // the row's elements are in registers, their stage is free
       at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
       if (kNorm) {
-        pre = row_stats<kV>(f, c.ok, a.norm, a.eps, a.inv, n, inv_n, t);
+        pre = row_stats<kV>(f, c, a.norm, a.eps, a.inv, n, inv_n, t);
         const f2 m = both(-pre.x), s = both(pre.y);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           f2 S[4], B[4];
-          get8(sS + c.at[j], half, S);
-          get8(sB + c.at[j], half, B);
+          get8(sS + c.at(j), half, S);
+          get8(sB + c.at(j), half, B);
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[j][i] = fma2(mul2(add2(f[j][i], m), s), S[i], B[i]);
-          if (c.ok[j]) put_row(h + c.col[j], f[j], a.wide);
+          if (c.ok(j)) put_row(h + c.col(j), f[j], a.wide);
+          one_by_one();
         }
         h += skip;
       }
@@ -538,7 +554,7 @@ __device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, lon
 template <typename TX, typename TY, int kV, int kR, int kThreads, bool kBranch, bool kNorm>
 __global__ void __launch_bounds__(kThreads, 1)
     gnorm_bwd_kernel(const __grid_constant__ GnArgs a) {
-  extern __shared__ __align__(16) char dyn[];
+  extern __shared__ __align__(128) char dyn[];
   __shared__ float4 red[2][kMaxWarps];
   const int nvec = a.C / 8;
   Team t;
@@ -550,27 +566,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   t.tid = threadIdx.x;
   t.red = red;
   t.buf = 0;
-  Cols<kV> c;
-  c.init(t, nvec);
-  Part<TX, kV> lx;
-  Part<TY, kV> ly;
-  lx.init(t, nvec);
-  ly.init(t, nvec);
+  Cols c(t, a.C);
+  Part<TX, kV> lx(t);
+  Part<TY, kV> ly(t);
   const int xb = Part<TX, kV>::bytes(t.threads), yb = Part<TY, kV>::bytes(t.threads);
-  const int o_y = a.gx ? xb : 0, o_x = o_y + (a.need_y ? yb : 0), o_gh = o_x + xb;
+  const int o_y = xb, o_x = o_y + (kBranch ? yb : 0), o_gh = o_x + xb;
   const int row_bytes = kNorm ? o_gh + yb : o_x, stage = kR * row_bytes;
   const int half = factor_half(nvec);
   char* const sG = dyn;
   char* const sS = sG + (kBranch ? 2 * half : 0);
-  char* const ring = sS + (kNorm ? 2 * half : 0);
+  char* const ring = dyn + up128(4 * half);
   const uint32_t ring_at = shared_u32(ring);
   const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
   const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
   const long long off = (long long)r0 * a.C;
   const TX* px = kNorm ? static_cast<const TX*>(a.x) + off : nullptr;
   const TY* pgh = kNorm ? static_cast<const TY*>(a.gh) + off : nullptr;
-  const TX* pgx = a.gx ? static_cast<const TX*>(a.gx) + off : nullptr;
-  const TY* py = a.need_y ? static_cast<const TY*>(a.y) + off : nullptr;
+  // gx and y may be absent: zeros, and the address of an output that is not read
+  const TX* pgx = static_cast<const TX*>(a.gx ? a.gx : a.dx) + off;
+  const TY* py = kBranch ? static_cast<const TY*>(a.need_y ? a.y : a.dy) + off : nullptr;
+  const bool have_gx = a.gx != nullptr, have_y = a.need_y;
   TX* dx = static_cast<TX*>(a.dx) + off;
   TY* dy = kBranch ? static_cast<TY*>(a.dy) + off : nullptr;
   long long g = r0 / a.group;
@@ -581,23 +596,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kR; ++k) {
         const uint32_t at = ring_at + to + k * row_bytes;
-        const bool on = k == 0 || ahead < ahead_end;
+        const bool on = k == 0 || ahead + k < ahead_end;
+        const long long e = on ? (long long)k * a.C : 0;
         if (kNorm) {
-          lx.fetch(at + o_x, px, on);
-          ly.fetch(at + o_gh, pgh, on);
+          lx.fetch(at + o_x, px + e, c, on);
+          ly.fetch(at + o_gh, pgh + e, c, on);
         }
-        if (a.gx) lx.fetch(at, pgx, on);
-        if (kBranch && a.need_y) ly.fetch(at + o_y, py, on);
-        if (on) {
-          if (kNorm) {
-            px += a.C;
-            pgh += a.C;
-          }
-          if (a.gx) pgx += a.C;
-          if (kBranch && a.need_y) py += a.C;
-          ++ahead;
-        }
+        lx.fetch(at, pgx + e, c, on && have_gx);
+        if (kBranch) ly.fetch(at + o_y, py + e, c, on && have_y);
       }
+      const int rows = min(kR, ahead_end - ahead);
+      const int step = rows * a.C;
+      if (kNorm) {
+        px += step;
+        pgh += step;
+      }
+      pgx += step;
+      if (kBranch) py += step;
+      ahead += rows;
       if (ahead == ahead_end) ahead_end = (int)min((long long)r1, ahead + a.group);
     }
     copy_commit();
@@ -630,12 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kV; ++j) {  // each thread reads the factors that it writes
         f2 p[4] = {0, 0, 0, 0}, q[4];
         if (kBranch) {
-          if (c.ok[j]) gate8(a, g, c.col[j], p);
-          put8(sG + c.at[j], half, p);
+          if (c.ok(j)) gate8(a, g, c.col(j), p);
+          put8(sG + c.at(j), half, p);
         }
         if (kNorm) {
-          if (c.ok[j]) scale8(a, g, c.col[j], p, q);
-          put8(sS + c.at[j], half, p);
+          if (c.ok(j)) scale8(a, g, c.col(j), p, q);
+          put8(sS + c.at(j), half, p);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum.a[j][i] = sum.s[j][i] = sum.d[j][i] = 0;
@@ -653,6 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     stats_of(r + rows);
     ring_wait(a.depth);
     __syncwarp();  // what the other lanes have copied
+    c.first = anew(c.first);
+    lx.first = anew(lx.first);
+    ly.first = anew(ly.first);
     const char* at = ring + at_stage;
     f2 xh[kR][kV][4], v[kR][kV][4];  // xh; a, then t, then e
     float2 c12[kR];
@@ -664,12 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
         f2 S[4];
-        get8(sS + c.at[j], half, S);
+        get8(sS + c.at(j), half, S);
 #pragma unroll
         for (int k = 0; k < kR; ++k) {
           const f2 m = both(-st[k].x), s = both(st[k].y);
-          Part<TX, kV>::take(at + k * row_bytes + o_x, j, t, xh[k][j]);
-          Part<TY, kV>::take(at + k * row_bytes + o_gh, j, t, v[k][j]);
+          lx.take(at + k * row_bytes + o_x, j, c, xh[k][j]);
+          ly.take(at + k * row_bytes + o_gh, j, c, v[k][j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             xh[k][j][i] = mul2(add2(xh[k][j][i], m), s);
@@ -679,11 +698,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             s1[k] = add2(s1[k], v[k][j][i]);
             s2[k] = fma2(v[k][j][i], xh[k][j][i], s2[k]);
           }
+          one_by_one();
         }
       }
 #pragma unroll
       for (int k = 0; k < kR; ++k) part[k] = make_float2(sum2(s1[k]), sum2(s2[k]));
       t.sums(part, c12);
+    }
+    f2 c1[kR], c2[kR], sk[kR];
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      if (!kNorm) c12[k] = make_float2(0.f, 0.f);
+      c1[k] = both(a.norm == BASA_NORM_LAYER ? -c12[k].x * a.inv : 0.f);
+      c2[k] = both(-c12[k].y * a.inv);
+      sk[k] = both(st[k].y);
     }
     f2 s1[kR], s2[kR];
 #pragma unroll
@@ -692,33 +720,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       f2 G[4];
-      if (kBranch) get8(sG + c.at[j], half, G);
+      if (kBranch) get8(sG + c.at(j), half, G);
 #pragma unroll
       for (int k = 0; k < kR; ++k) {
         const char* row = at + k * row_bytes;
-        f2 gx[4] = {0, 0, 0, 0};
-        if (a.gx) Part<TX, kV>::take(row, j, t, gx);
+        f2 gx[4];
+        lx.take(row, j, c, gx);
         if (kNorm) {  // rstd (a - mean(a) - xh mean(a xh)) + gx
-          const f2 s = both(st[k].y);
-          const f2 c1 = both(a.norm == BASA_NORM_LAYER ? -c12[k].x * a.inv : 0.f),
-                   c2 = both(-c12[k].y * a.inv);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            gx[i] = fma2(s, fma2(xh[k][j][i], c2, add2(v[k][j][i], c1)), gx[i]);
+            gx[i] = fma2(sk[k], fma2(xh[k][j][i], c2[k], add2(v[k][j][i], c1[k])), gx[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[k][j][i] = mul2(res, gx[i]);
-        if (c.ok[j] && on[k]) put_row(dx + k * a.C + c.col[j], v[k][j], a.wide);
+        if (c.ok(j) && on[k]) put_row(dx + k * a.C + c.col(j), v[k][j], a.wide);
         if (kBranch) {
-          f2 yh[4] = {0, 0, 0, 0};
-          if (a.need_y) Part<TY, kV>::take(row + o_y, j, t, yh);
+          f2 yh[4];
+          ly.take(row + o_y, j, c, yh);
           if (a.post == BASA_NORM_NONE) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               sum.d[j][i] = fma2(gx[i], yh[i], sum.d[j][i]);
               v[k][j][i] = mul2(gx[i], G[i]);
             }
-            if (c.ok[j] && on[k]) put_row(dy + k * a.C + c.col[j], v[k][j], a.wide);
+            if (c.ok(j) && on[k]) put_row(dy + k * a.C + c.col(j), v[k][j], a.wide);
           } else {
             const f2 pm = both(-st[k].z), ps = both(st[k].w);
 #pragma unroll
@@ -731,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        one_by_one();
       }
     }
     if (kBranch && a.post != BASA_NORM_NONE) {
@@ -746,11 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           f2 yh[4];
-          Part<TY, kV>::take(at + k * row_bytes + o_y, j, t, yh);
+          ly.take(at + k * row_bytes + o_y, j, c, yh);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[k][j][i] = mul2(ps, fma2(mul2(add2(yh[i], pm), ps), c2, add2(v[k][j][i], c1)));
-          if (c.ok[j] && on[k]) put_row(dy + k * a.C + c.col[j], v[k][j], a.wide);
+          if (c.ok(j) && on[k]) put_row(dy + k * a.C + c.col(j), v[k][j], a.wide);
         }
       }
     }
@@ -902,7 +928,7 @@ basa_status go_fwd_v(GnArgs a, cudaStream_t st) {
   const int sms = row_sm_count();
   const unsigned grid = (unsigned)(a.rows < sms ? a.rows : sms);
   const long long most = (a.rows + grid - 1) / grid;  // rows of a CTA
-  const int factors = ((branch ? 1 : 0) + (norm ? 2 : 0)) * 2 * factor_half(a.C / 8);
+  const int factors = up128(((branch ? 1 : 0) + (norm ? 2 : 0)) * 2 * factor_half(a.C / 8));
   a.teams = kFwdThreads / per_row;
   if (a.warps > 1 && a.teams > 15) a.teams = 15;  // barriers of a CTA
   if (a.teams > most) a.teams = (int)most;
@@ -921,35 +947,33 @@ basa_status go_fwd_v(GnArgs a, cudaStream_t st) {
 template <typename TX, typename TY>
 basa_status go_fwd(GnArgs a, cudaStream_t st) {
   const int nvec = a.C / 8;
-  a.warps = (nvec + 127) / 128;
+  a.warps = (nvec + 159) / 160;
   const int v = (nvec + 32 * a.warps - 1) / (32 * a.warps);
-  return v == 4   ? go_fwd_v<TX, TY, 4>(a, st)
+  return v == 5   ? go_fwd_v<TX, TY, 5>(a, st)
+         : v == 4 ? go_fwd_v<TX, TY, 4>(a, st)
          : v == 3 ? go_fwd_v<TX, TY, 3>(a, st)
          : v == 2 ? go_fwd_v<TX, TY, 2>(a, st)
                   : go_fwd_v<TX, TY, 1>(a, st);
 }
 
-// Launch shape of the backward.  Two vectors a thread (their sums: 48 registers)
-// and two rows at a time up to 320 threads (168 registers each); beyond, rows of
-// more than 5120 columns, one row at a time.
+// Launch shape of the backward.  Up to 640 threads, one vector and two rows a
+// thread; wider rows, of more than 5120 columns, two vectors and one row.  At
+// 16384 rows of 5120 bf16 columns: one vector and two rows 189 us, two vectors
+// and two rows (half the warps) 199, one and one 215.
 struct BwdShape {
-  int threads, rows, per_sm, bytes;  // bytes: shared memory beside the ring; rows at a time
+  int v, threads, per_sm, bytes;  // bytes: shared memory beside the ring
   long long grid;
 };
-constexpr int kBwdV = 2, kBwdThreads = 320;
-int bwd_row_bytes(const basa_gnorm_params* p, int threads) {
-  const int sx = p->x_dtype == BASA_BF16 ? 2 : 4, sy = p->dtype == BASA_BF16 ? 2 : 4;
-  return kBwdV * threads * 8 * 2 * (sx + sy);
-}
 BwdShape bwd_shape(const basa_gnorm_params* p) {
   BwdShape s;
-  const int nvec = p->C / 8;
-  s.threads = round32((nvec + kBwdV - 1) / kBwdV);
-  s.rows = s.threads <= kBwdThreads ? 2 : 1;
-  s.bytes = 4 * factor_half(nvec);
-  const int need = s.bytes + s.rows * bwd_row_bytes(p, s.threads) + 2048;
-  s.per_sm = (s.threads <= kBwdThreads ? kBwdThreads : 512) / s.threads;
-  if (s.per_sm > kSmem / need) s.per_sm = kSmem / need;
+  const int nvec = p->C / 8, most = nvec <= 640 ? 640 : 512;
+  s.v = nvec <= 640 ? 1 : 2;
+  s.threads = round32((nvec + s.v - 1) / s.v);
+  s.bytes = up128(4 * factor_half(nvec));
+  const int sx = p->x_dtype == BASA_BF16 ? 2 : 4, sy = p->dtype == BASA_BF16 ? 2 : 4;
+  const int stage = 2 * s.threads * 8 * 2 * (sx + sy);  // 1 x 2 or 2 x 1 vectors of four rows
+  s.per_sm = most / s.threads;
+  if (s.per_sm > kSmem / (s.bytes + stage + 2048)) s.per_sm = kSmem / (s.bytes + stage + 2048);
   if (s.per_sm > 8) s.per_sm = 8;
   if (s.per_sm < 1) s.per_sm = 1;
   long long cap = (long long)row_sm_count() * s.per_sm;
@@ -965,28 +989,25 @@ size_t part_w_bytes(const basa_gnorm_params* p, const BwdShape& s) {
   return up256((size_t)s.grid * 3 * p->C * sizeof(float));
 }
 
-template <typename TX, typename TY, int kR, int kThreads>
+template <typename TX, typename TY, int kV, int kR, int kThreads>
 basa_status go_bwd_t(GnArgs a, const BwdShape& s, cudaStream_t st) {
   const bool branch = a.dy != nullptr, norm = a.norm != BASA_NORM_NONE;
-  const int xb = Part<TX, kBwdV>::bytes(s.threads), yb = Part<TY, kBwdV>::bytes(s.threads);
-  const int stage = kR * ((a.gx ? xb : 0) + (a.need_y ? yb : 0) + (norm ? xb + yb : 0));
+  const int xb = Part<TX, kV>::bytes(s.threads), yb = Part<TY, kV>::bytes(s.threads);
+  const int stage = kR * (xb + (branch ? yb : 0) + (norm ? xb + yb : 0));
   a.depth = (kSmem / s.per_sm - 2048 - s.bytes) / stage;
   a.depth = a.depth > 3 ? 3 : a.depth < 1 ? 1 : a.depth;
   const int smem = s.bytes + a.depth * stage;
   const unsigned grid = (unsigned)s.grid;
   if (branch && norm)
-    return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, true, true>, a, grid, s.threads, smem,
-              st);
+    return go(gnorm_bwd_kernel<TX, TY, kV, kR, kThreads, true, true>, a, grid, s.threads, smem, st);
   if (branch)
-    return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, true, false>, a, grid, s.threads, smem,
+    return go(gnorm_bwd_kernel<TX, TY, kV, kR, kThreads, true, false>, a, grid, s.threads, smem,
               st);
-  return go(gnorm_bwd_kernel<TX, TY, kBwdV, kR, kThreads, false, true>, a, grid, s.threads, smem,
-            st);
+  return go(gnorm_bwd_kernel<TX, TY, kV, kR, kThreads, false, true>, a, grid, s.threads, smem, st);
 }
 template <typename TX, typename TY>
 basa_status go_bwd(const GnArgs& a, const BwdShape& s, cudaStream_t st) {
-  return s.rows == 2 ? go_bwd_t<TX, TY, 2, kBwdThreads>(a, s, st)
-                     : go_bwd_t<TX, TY, 1, 512>(a, s, st);
+  return s.v == 1 ? go_bwd_t<TX, TY, 1, 2, 640>(a, s, st) : go_bwd_t<TX, TY, 2, 1, 512>(a, s, st);
 }
 
 }  // namespace

@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(RopeArgs a) 
   int fh = h0, to = 0;
   auto fetch = [&]() {
     if (fn < a.tokens) {
-      if (fh < hend) {
-        Slot<TI>::fetch(ring + to, x + fh * kD + l.ea, 0, 32, lane);
-        Slot<TI>::fetch(ring + to, x + fh * kD + l.eb, 1, 32, lane);
-      }
+      const bool on = fh < hend;
+      const TI* head = x + (on ? fh : 0) * kD;
+      Slot<TI>::fetch(ring + to, head + l.ea, 0, 32, lane, on);
+      Slot<TI>::fetch(ring + to, head + l.eb, 1, 32, lane, on);
       fh += kHpw;
       if (fh - slot >= hend) {
         fh = h0;
@@ -363,12 +363,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(RopeArgs a) 
       fetch();
       copy_wait<kDepth - 1>();
       Raw8<TI> ra, rb;
-      zero8(ra);
-      zero8(rb);
-      if (h < hend) {
-        Slot<TI>::take(rings[warp] + from, 0, 32, lane, ra);
-        Slot<TI>::take(rings[warp] + from, 1, 32, lane, rb);
-      }
+      Slot<TI>::take(rings[warp] + from, 0, 32, lane, ra);
+      Slot<TI>::take(rings[warp] + from, 1, 32, lane, rb);
       from = from + kStage == kDepth * kStage ? 0 : from + kStage;
       f2 A[4], B[4];
       unpack16<kHalves>(ra, rb, A, B);
@@ -429,13 +425,13 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
   int fh = h0, to = 0;
   auto fetch = [&]() {
     if (fn < a.tokens) {
-      if (fh < hend) {
-        Slot<T>::fetch(ring + to, g + fh * kD + l.ea, 0, 32, lane);
-        Slot<T>::fetch(ring + to, g + fh * kD + l.eb, 1, 32, lane);
-        if (kNorm) {
-          Slot<T>::fetch(ring + to, x + fh * kD + l.ea, 2, 32, lane);
-          Slot<T>::fetch(ring + to, x + fh * kD + l.eb, 3, 32, lane);
-        }
+      const bool on = fh < hend;
+      const int head = (on ? fh : 0) * kD;
+      Slot<T>::fetch(ring + to, g + head + l.ea, 0, 32, lane, on);
+      Slot<T>::fetch(ring + to, g + head + l.eb, 1, 32, lane, on);
+      if (kNorm) {
+        Slot<T>::fetch(ring + to, x + head + l.ea, 2, 32, lane, on);
+        Slot<T>::fetch(ring + to, x + head + l.eb, 3, 32, lane, on);
       }
       fh += kHpw;
       if (fh - slot >= hend) {
@@ -461,33 +457,28 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
     ang.put(cs[warp][buf], lane, 32);
     __syncwarp();
     ang.ahead(a);
-    f2 C[4], S[4];
+    f2 C[4], S[4], N[4];  // N = -S
     angles_of(cs[warp][buf], l, C, S);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) N[i] = neg2(S[i]);
     for (int h = h0; h - slot < hend; h += kHpw) {  // the same trip count for a warp
-      const bool on = h < hend;
       fetch();
       copy_wait<kDepth - 1>();
       const char* at = rings[warp] + from;
       from = from + kStage == kDepth * kStage ? 0 : from + kStage;
       f2 A[4], B[4], GA[4], GB[4];
       Raw8<T> ra, rb;
-      zero8(ra);
-      zero8(rb);
-      if (on) {
-        Slot<T>::take(at, 0, 32, lane, ra);
-        Slot<T>::take(at, 1, 32, lane, rb);
-      }
+      Slot<T>::take(at, 0, 32, lane, ra);
+      Slot<T>::take(at, 1, 32, lane, rb);
       unpack16<kHalves>(ra, rb, A, B);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // turned back
         GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
-        GB[i] = fma2(B[i], C[i], neg2(mul2(A[i], S[i])));
+        GB[i] = fma2(B[i], C[i], mul2(A[i], N[i]));
       }
       if (kNorm) {
-        if (on) {
-          Slot<T>::take(at, 2, 32, lane, ra);
-          Slot<T>::take(at, 3, 32, lane, rb);
-        }
+        Slot<T>::take(at, 2, 32, lane, ra);
+        Slot<T>::take(at, 3, 32, lane, rb);
         unpack16<kHalves>(ra, rb, A, B);
         f2 s0 = mul2(A[0], A[0]), s1 = mul2(B[0], B[0]);
         f2 d0 = mul2(A[0], mul2(GA[0], WA[0])), d1 = mul2(B[0], mul2(GB[0], WB[0]));
@@ -512,7 +503,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
           GB[i] = fma2(pB, WB[i], mul2(B[i], cc));
         }
       }
-      if (on) pack16<kHalves>(o + h * kD, l, GA, GB);
+      if (h < hend) pack16<kHalves>(o + h * kD, l, GA, GB);
     }
   }
   if (kNorm && P.part) {  // uniform over the CTA
@@ -607,7 +598,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
   const int h0 = tid / lph * a.d, dh = threads / lph * a.d;  // a thread's heads, in elements
   const uint32_t stride = gridDim.x;
   uint32_t n = blockIdx.x, fn = n;
-  const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx + h0;
+  const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx;
   TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo + h0;
   const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
   bool on[kV];
@@ -621,11 +612,11 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
   auto fetch = [&]() {
     if (fn < a.tokens) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        if (on[j]) {
-          Slot<TI>::fetch(ring_at + to, x + j * dh + l.ea, 2 * j, threads, tid);
-          Slot<TI>::fetch(ring_at + to, x + j * dh + l.eb, 2 * j + 1, threads, tid);
-        }
+      for (int j = 0; j < kV; ++j) {
+        const TI* head = x + (on[j] ? h0 + j * dh : 0);
+        Slot<TI>::fetch(ring_at + to, head + l.ea, 2 * j, threads, tid, on[j]);
+        Slot<TI>::fetch(ring_at + to, head + l.eb, 2 * j + 1, threads, tid, on[j]);
+      }
       fn += stride;
       x += dx;
     }
@@ -634,12 +625,8 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
   };
   auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
     Raw8<TI> ra, rb;
-    zero8(ra);
-    zero8(rb);
-    if (on[j]) {
-      Slot<TI>::take(ring + from, 2 * j, threads, tid, ra);
-      Slot<TI>::take(ring + from, 2 * j + 1, threads, tid, rb);
-    }
+    Slot<TI>::take(ring + from, 2 * j, threads, tid, ra);
+    Slot<TI>::take(ring + from, 2 * j + 1, threads, tid, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
 #pragma unroll
@@ -691,11 +678,12 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
     from = from + stage == kDepth * stage ? 0 : from + stage;
     const float r = mul * rsqrtf(block_sum(sum2(s), sm, buf) * inv + a.eps);
     const f2 rr = pk(r, r);
-    f2 C[4], S[4];
+    f2 C[4], S[4], N[4];  // N = -S
     angles_of(sm.cs[buf], l, C, S);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       C[i] = mul2(C[i], rr);
+      N[i] = mul2(S[i], pk(-r, -r));
       S[i] = mul2(S[i], rr);
     }
 #pragma unroll
@@ -705,7 +693,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 p = mul2(A[j][i], WA[i]), q = mul2(B[j][i], WB[i]);
-        A[j][i] = fma2(p, C[i], neg2(mul2(q, S[i])));
+        A[j][i] = fma2(p, C[i], mul2(q, N[i]));
         B[j][i] = fma2(q, C[i], mul2(p, S[i]));
       }
       if (on[j]) pack16<kHalves>(o + j * dh, l, A[j], B[j]);
@@ -725,8 +713,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
   const int lph = a.d / 16, tid = threadIdx.x, threads = blockDim.x;
   const float inv = 1.f / (float)(P.heads * a.d);
   const Lane l = lane_of<kHalves>(a, tid % lph);
-  const int h0 = tid / lph * a.d;
   const bool on = tid < P.heads * lph;
+  const int h0 = on ? tid / lph * a.d : 0;
   const uint32_t stride = gridDim.x;
   uint32_t n = blockIdx.x, fn = n;
   const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg + h0;
@@ -740,12 +728,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
   const uint32_t ring_at = shared_u32(ring);
   int to = 0, from = 0;
   auto fetch = [&]() {
-    if (fn < a.tokens && on) {
-      Slot<T>::fetch(ring_at + to, g + l.ea, 0, threads, tid);
-      Slot<T>::fetch(ring_at + to, g + l.eb, 1, threads, tid);
+    if (fn < a.tokens) {
+      Slot<T>::fetch(ring_at + to, g + l.ea, 0, threads, tid, on);
+      Slot<T>::fetch(ring_at + to, g + l.eb, 1, threads, tid, on);
       if (part < 2) {
-        Slot<T>::fetch(ring_at + to, x + l.ea, 2, threads, tid);
-        Slot<T>::fetch(ring_at + to, x + l.eb, 3, threads, tid);
+        Slot<T>::fetch(ring_at + to, x + l.ea, 2, threads, tid, on);
+        Slot<T>::fetch(ring_at + to, x + l.eb, 3, threads, tid, on);
       }
     }
     fn += stride;  // at most twice the CTAs past the tokens, far from 2^32
@@ -762,12 +750,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
   };
   auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
     Raw8<T> ra, rb;
-    zero8(ra);
-    zero8(rb);
-    if (on) {
-      Slot<T>::take(ring + from, j, threads, tid, ra);
-      Slot<T>::take(ring + from, j + 1, threads, tid, rb);
-    }
+    Slot<T>::take(ring + from, j, threads, tid, ra);
+    Slot<T>::take(ring + from, j + 1, threads, tid, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
   if (depth == 2) fetch();
@@ -806,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
-        GB[i] = fma2(B[i], C[i], neg2(mul2(A[i], S[i])));
+        GB[i] = fma2(B[i], C[i], mul2(A[i], neg2(S[i])));
       }
       take(2, XA, XB);
       get_weights(weights, 0, A, B);

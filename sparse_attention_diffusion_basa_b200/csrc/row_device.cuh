@@ -132,8 +132,11 @@ __device__ __forceinline__ void store8(T* o, const f2 (&p)[4]) {
 // stages need no barrier.  A slot holds one tensor's vectors of a stage, in
 // 16-byte pieces, the threads side by side.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// on = false: sixteen bytes of zeros, and src, any valid address, is not read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -151,11 +154,11 @@ struct Slot {
     return vectors * kPieces * threads * 16;
   }
   __device__ static __forceinline__ void fetch(uint32_t at, const T* src, int j, int threads,
-                                               int tid) {
+                                               int tid, bool on) {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p)
       copy16(at + ((j * kPieces + p) * threads + tid) * 16,
-             reinterpret_cast<const char*>(src) + p * 16);
+             reinterpret_cast<const char*>(src) + p * 16, on);
   }
   __device__ static __forceinline__ void take(const char* at, int j, int threads, int tid,
                                               Raw8<T>& r) {
