@@ -10,6 +10,7 @@ tensors' device, or on ``stream``; what it allocates belongs to that stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -19,6 +20,28 @@ from ._lib import (BASA_BF16, BASA_F32, BASA_FP8_E4M3, BASA_NORM, BASA_ROPE_LAYO
                    BasaGnormParams, BasaRopeParams)
 
 _DT = {torch.float32: BASA_F32, torch.bfloat16: BASA_BF16, torch.float8_e4m3fn: BASA_FP8_E4M3}
+_FLOAT = (torch.float32, torch.bfloat16)
+_E4M3 = torch.float8_e4m3fn
+
+# The small calls of a sampler are bound by this file, not by their kernels, so
+# the checks of a call's shapes, strides, types and devices and the parameter
+# struct they lead to are kept (lru_cache) by just these: never by a tensor, its
+# address or its values.
+_KEPT = 512
+
+
+def _meta(t):
+    """What the checks look at: (shape, strides, dtype, device), or None."""
+    if t is None:
+        return None
+    try:
+        return t.shape, t.stride(), t.dtype, t.device
+    except AttributeError:
+        raise TypeError(f"expected a torch tensor, got {type(t).__name__}") from None
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _code(table, key, name):
@@ -28,51 +51,74 @@ def _code(table, key, name):
         raise ValueError(f"{name} must be one of {sorted(map(str, table))}, got {key!r}") from None
 
 
-def _on(t: torch.Tensor, fn, what: str, *args):
-    """Calls ``fn`` with t's device current and its stream as the last argument."""
-    dev = t.device
-    if torch.cuda.current_device() == dev.index:
-        _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), what)
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on(device, fn, what: str, *args):
+    """Calls ``fn`` with ``device`` current and its current stream as the last argument."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            _lib.check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), what)
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        _lib.check(code, what)
 
 
-def _size(t: torch.Tensor, fn, prm) -> int:
-    """Workspace bytes, asked with t's device current (they go by its SMs)."""
-    if torch.cuda.current_device() == t.device.index:
-        return int(fn(ctypes.byref(prm)))
-    with torch.cuda.device(t.device):
-        return int(fn(ctypes.byref(prm)))
+@functools.lru_cache(maxsize=_KEPT)
+def _size(device, name, ref) -> int:
+    """Workspace bytes for a plan's struct, asked with ``device`` current (they go by its SMs)."""
+    with torch.cuda.device(device.index):
+        return int(getattr(_lib.load(), name)(ref.params))
 
 
-def _workspace(t, need, workspace):
+def _workspace(device, need, workspace):
     if not need:
         return None
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=t.device)
-    if workspace.device != t.device or not workspace.is_contiguous() or \
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace must hold {need} contiguous bytes on {t.device}")
+        raise ValueError(f"workspace must hold {need} contiguous bytes on {device}")
     return workspace
 
 
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+class _Plan:
+    """A checked call: its parameter struct (as passed) and what the call allocates by."""
+
+    def __init__(self, struct, **kw):
+        self.struct, self.params = struct, ctypes.byref(struct)
+        self.__dict__.update(kw)
 
 
-def _tensor(t, ref, name, dtypes):
-    if not isinstance(t, torch.Tensor):
+def _tensor(m, ref, name, dtypes):
+    if m is None:
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
+    if m[3].type != "cuda":
         raise ValueError(f"{name} must be on a CUDA device")
-    if ref is not None and t.device != ref.device:
-        raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if ref is not None and m[3] != ref[3]:
+        raise ValueError(f"{name} must be on {ref[3]}, got {m[3]}")
+    if m[2] not in dtypes:
+        raise TypeError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, got {m[2]}")
 
 
-_FLOAT = (torch.float32, torch.bfloat16)
+def _numel(shape):
+    n = 1
+    for s in shape:
+        n *= s
+    return n
+
+
+def _dense(m) -> bool:
+    expect = 1
+    for size, st in zip(reversed(m[0]), reversed(m[1])):
+        if size != 1:
+            if st != expect:
+                return _numel(m[0]) == 0
+            expect *= size
+    return True
 
 
 def _row_stride(shape, stride, n, name) -> int:
@@ -92,21 +138,19 @@ def _row_stride(shape, stride, n, name) -> int:
 # ---------------------------------------------------------------------------
 # q/k/v preparation
 # ---------------------------------------------------------------------------
-def _heads(t, ref, name, dtypes, dense=False) -> int:
+def _heads(m, ref, name, dtypes, dense=False) -> int:
     """Checks a [B, T, Hg, Wg, heads, d] (or text [B, L, heads, d]) tensor; its row stride, 0 = dense."""
-    _tensor(t, ref, name, dtypes)
-    if t.dim() not in (4, 6):
-        raise ValueError(f"{name} must be [B, T, Hg, Wg, heads, d] or [B, L, heads, d], got {tuple(t.shape)}")
-    if t.is_contiguous():
+    _tensor(m, ref, name, dtypes)
+    shape, stride = m[0], m[1]
+    if len(shape) not in (4, 6):
+        raise ValueError(f"{name} must be [B, T, Hg, Wg, heads, d] or [B, L, heads, d], got {tuple(shape)}")
+    if _dense(m):
         return 0
     if dense:
         raise ValueError(f"{name} must be contiguous")
-    shape, stride = t.shape, t.stride()
-    if t.numel() == 0:
-        return 0
     if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
         raise ValueError(f"the heads of {name} must be dense, got strides {tuple(stride)}")
-    ld = _row_stride(shape, stride, t.dim() - 2, name)
+    ld = _row_stride(shape, stride, len(shape) - 2, name)
     if ld is None:
         return 0
     if ld < shape[-1] * shape[-2]:
@@ -115,16 +159,16 @@ def _heads(t, ref, name, dtypes, dense=False) -> int:
 
 
 def _rope_params(q, k, axes, layout, norm, eps, out_dtype, descale, lds, w_dtype) -> BasaRopeParams:
-    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
-        raise ValueError(f"k {tuple(k.shape)} must match q {tuple(q.shape)} except in heads")
-    H, Hkv = q.shape[-2], k.shape[-2]
+    q, k, dtype = q[0], k[0], q[2]
+    if k[:-2] != q[:-2] or k[-1] != q[-1]:
+        raise ValueError(f"k {tuple(k)} must match q {tuple(q)} except in heads")
+    H, Hkv = q[-2], k[-2]
     if H != Hkv and (Hkv == 0 or H % Hkv):
         raise ValueError(f"q heads {H} must be a multiple of k/v heads {Hkv}")
-    B = q.shape[0]
-    T, Hg, Wg = q.shape[1:4] if q.dim() == 6 else (1, 1, q.shape[1])
+    T, Hg, Wg = q[1:4] if len(q) == 6 else (1, 1, q[1])
     at, ah, aw = (int(a) for a in axes)
-    return BasaRopeParams(B, H, Hkv, T, Hg, Wg, q.shape[-1], at, ah, aw, _code(BASA_ROPE_LAYOUT, layout, "layout"),
-                          _code(BASA_ROPE_NORM, norm, "norm"), float(eps), _DT[q.dtype], _DT[out_dtype],
+    return BasaRopeParams(q[0], H, Hkv, T, Hg, Wg, q[-1], at, ah, aw, _code(BASA_ROPE_LAYOUT, layout, "layout"),
+                          _code(BASA_ROPE_NORM, norm, "norm"), float(eps), _DT[dtype], _DT[out_dtype],
                           _DT[w_dtype], *(float(x) for x in descale), *lds)
 
 
@@ -132,15 +176,16 @@ def _pairs(prm) -> int:
     return prm.T * (prm.at // 2) + prm.Hg * (prm.ah // 2) + prm.Wg * (prm.aw // 2)
 
 
-def _check_table(table, q, prm):
+def _check_table(table, q, prm) -> bool:
+    """Whether the call turns anything; then the table has to fit."""
     n = _pairs(prm)
     if n == 0:
-        return None
+        return False
     _tensor(table, q, "table", (torch.float32,))
-    if table.numel() != 2 * n or not table.is_contiguous():
+    if _numel(table[0]) != 2 * n or not _dense(table):
         raise ValueError(f"table must hold {n} contiguous (cos, sin) pairs for this grid and these axes, "
-                         f"got {tuple(table.shape)}")
-    return table
+                         f"got {tuple(table[0])}")
+    return True
 
 
 def _weights(q, k, q_weight, k_weight, norm):
@@ -152,13 +197,26 @@ def _weights(q, k, q_weight, k_weight, norm):
         if norm is None:
             raise ValueError(f"{name} needs a norm")
         _tensor(w, q, name, _FLOAT)
-        n = t.shape[-1] * (t.shape[-2] if norm == "token" else 1)
-        if w.numel() != n or not w.is_contiguous():
-            raise ValueError(f"{name} must be {n} contiguous values, got {tuple(w.shape)}")
-        if dtype not in (None, w.dtype):
+        n = t[0][-1] * (t[0][-2] if norm == "token" else 1)
+        if _numel(w[0]) != n or not _dense(w):
+            raise ValueError(f"{name} must be {n} contiguous values, got {tuple(w[0])}")
+        if dtype not in (None, w[2]):
             raise TypeError("q_weight and k_weight must share a dtype")
-        dtype = w.dtype
+        dtype = w[2]
     return dtype or torch.float32
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _table_plan(grid, axes, out):
+    T, Hg, Wg = (int(g) for g in grid)
+    at, ah, aw = (int(a) for a in axes)
+    d = 32
+    while d < at + ah + aw and d < 128:
+        d *= 2
+    prm = BasaRopeParams(1, 1, 1, T, Hg, Wg, d, at, ah, aw, 0, 0, 1.0, BASA_F32, BASA_F32, BASA_F32)
+    if out is not None:
+        _check_table(out, out, prm)
+    return _Plan(prm, pairs=max(_pairs(prm), 0))
 
 
 def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0),
@@ -171,23 +229,40 @@ def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(
     if stream is not None:
         with torch.cuda.stream(stream):
             return rope_table(grid, axes, theta, start, step, device, out)
-    T, Hg, Wg = (int(g) for g in grid)
-    at, ah, aw = (int(a) for a in axes)
-    d = 32
-    while d < at + ah + aw and d < 128:
-        d *= 2
-    prm = BasaRopeParams(1, 1, 1, T, Hg, Wg, d, at, ah, aw, 0, 0, 1.0, BASA_F32, BASA_F32, BASA_F32)
-    lib = _lib.load()
-    pos = [(ctypes.c_double * 3)(*(float(x) for x in v)) for v in (start, step)]
+    plan = _table_plan(tuple(grid), tuple(axes), _meta(out))
     if out is None:
         dev = torch.device("cuda" if device is None else device)
         if dev.type != "cuda":
             raise ValueError("device must be a CUDA device")
-        out = torch.empty((max(_pairs(prm), 0), 2), dtype=torch.float32, device=dev)
-    else:
-        _check_table(out, out, prm)
-    _on(out, lib.basa_rope_table, "basa_rope_table", _p(out), float(theta), *pos, ctypes.byref(prm))
+        out = torch.empty((plan.pairs, 2), dtype=torch.float32, device=dev)
+    d3 = ctypes.c_double * 3
+    _on(out.device, _lib.load().basa_rope_table, "basa_rope_table", out.data_ptr(), float(theta), d3(*start),
+        d3(*step), plan.params)
     return out
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _rope_plan(q, k, v, q_weight, k_weight, table, out, axes, layout, norm, eps, out_dtype, descale):
+    lds = [_heads(q, None, "q", _FLOAT), _heads(k, q, "k", (q[2],)), 0]
+    if v is not None:
+        lds[2] = _heads(v, q, "v", (q[2],))
+        if v[0] != k[0]:
+            raise ValueError("k and v must have the same shape")
+    dt = q[2] if out_dtype is None else out_dtype
+    if dt not in (q[2], _E4M3):
+        raise TypeError(f"out_dtype must be {q[2]} or {_E4M3}, got {dt}")
+    w_dtype = _weights(q, k, q_weight, k_weight, norm)
+    prm = _rope_params(q, k, axes, layout, norm, eps, dt, descale, lds, w_dtype)
+    turns = _check_table(table, q, prm)
+    if out is not None:
+        for o, t, name in zip(out, (q, k, v), "qkv"):
+            if (o is None) != (t is None):
+                raise ValueError(f"out must give {name}'s output exactly when {name} is given")
+            if o is not None:
+                _heads(o, q, f"{name}'s output", (dt,), dense=True)
+                if o[0] != t[0]:
+                    raise ValueError(f"{name}'s output must have shape {tuple(t[0])}")
+    return _Plan(prm, dtype=dt, turns=turns)
 
 
 def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=None, q_weight=None,
@@ -207,32 +282,49 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
         with torch.cuda.stream(stream):
             return qkv_rope(q, k, v, table, axes, layout=layout, norm=norm, q_weight=q_weight, k_weight=k_weight,
                             eps=eps, out_dtype=out_dtype, descale=descale, out=out)
-    lds = [_heads(q, None, "q", _FLOAT), _heads(k, q, "k", (q.dtype,)), 0]
-    if v is not None:
-        lds[2] = _heads(v, q, "v", (q.dtype,))
-        if v.shape != k.shape:
-            raise ValueError("k and v must have the same shape")
-    dt = q.dtype if out_dtype is None else out_dtype
-    if dt not in (q.dtype, torch.float8_e4m3fn):
-        raise TypeError(f"out_dtype must be {q.dtype} or torch.float8_e4m3fn, got {dt}")
-    w_dtype = _weights(q, k, q_weight, k_weight, norm)
-    prm = _rope_params(q, k, axes, layout, norm, eps, dt, descale, lds, w_dtype)
-    table = _check_table(table, q, prm)
+    outs = None if out is None else tuple(_meta(o) for o in out)
+    plan = _rope_plan(_meta(q), _meta(k), _meta(v), _meta(q_weight), _meta(k_weight), _meta(table), outs,
+                      tuple(axes), layout, norm, eps, out_dtype, tuple(descale))
+    dev = q.device
     if out is None:
-        qo, ko = torch.empty(q.shape, dtype=dt, device=q.device), torch.empty(k.shape, dtype=dt, device=q.device)
-        vo = None if v is None else torch.empty(k.shape, dtype=dt, device=q.device)
+        dt = plan.dtype
+        qo, ko = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+        vo = None if v is None else torch.empty(k.shape, dtype=dt, device=dev)
     else:
         qo, ko, vo = out
-        for o, t, name in ((qo, q, "q"), (ko, k, "k"), (vo, v, "v")):
-            if (o is None) != (t is None):
-                raise ValueError(f"out must give {name}'s output exactly when {name} is given")
-            if o is not None:
-                _heads(o, q, f"{name}'s output", (dt,), dense=True)
-                if o.shape != t.shape:
-                    raise ValueError(f"{name}'s output must have shape {tuple(t.shape)}")
-    _on(q, _lib.load().basa_qkv_rope, "basa_qkv_rope", _p(q), _p(k), _p(v), _p(q_weight), _p(k_weight), _p(table),
-        _p(qo), _p(ko), _p(vo), ctypes.byref(prm))
+    _on(dev, _lib.load().basa_qkv_rope, "basa_qkv_rope", q.data_ptr(), k.data_ptr(), _p(v), _p(q_weight),
+        _p(k_weight), table.data_ptr() if plan.turns else None, qo.data_ptr(), ko.data_ptr(), _p(vo), plan.params)
     return qo, ko, vo
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _rope_bwd_plan(dq_out, dk_out, dv_out, q, k, q_weight, k_weight, table, out, axes, layout, norm, eps):
+    _heads(dq_out, None, "dq_out", _FLOAT, dense=True)
+    dtypes = (dq_out[2],)
+    _heads(dk_out, dq_out, "dk_out", dtypes, dense=True)
+    lds = [0] * 6
+    for i, (t, g, name) in enumerate(((q, dq_out, "q"), (k, dk_out, "k"))):
+        if norm is None and t is None:
+            continue
+        lds[i] = _heads(t, dq_out, name, dtypes)
+        if t[0] != g[0]:
+            raise ValueError(f"{name} {tuple(t[0])} must have the shape of its output's gradient {tuple(g[0])}")
+    if dv_out is not None:
+        _heads(dv_out, dq_out, "dv_out", dtypes, dense=True)
+        if dv_out[0] != dk_out[0]:
+            raise ValueError("dk_out and dv_out must have the same shape")
+    if out is not None:
+        for i, (o, g) in enumerate(zip(out, (dq_out, dk_out, dv_out))):
+            if (o is None) != (g is None):
+                raise ValueError("out must give dv exactly when dv_out is given")
+            if o is not None:
+                lds[3 + i] = _heads(o, dq_out, "a gradient", dtypes)
+                if o[0] != g[0]:
+                    raise ValueError(f"a gradient must have shape {tuple(g[0])}, got {tuple(o[0])}")
+    w_dtype = _weights(dq_out, dk_out, q_weight, k_weight, norm)
+    prm = _rope_params(dq_out, dk_out, axes, layout, norm, eps, dq_out[2], (0.0, 0.0, 0.0), lds, w_dtype)
+    turns = _check_table(table, dq_out, prm)
+    return _Plan(prm, turns=turns)
 
 
 def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, layout="pairs", norm=None,
@@ -246,45 +338,25 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
         with torch.cuda.stream(stream):
             return qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table, axes, layout=layout, norm=norm,
                                 q_weight=q_weight, k_weight=k_weight, eps=eps, out=out, workspace=workspace)
-    _heads(dq_out, None, "dq_out", _FLOAT, dense=True)
-    _heads(dk_out, dq_out, "dk_out", (dq_out.dtype,), dense=True)
-    lds = [0] * 6
-    for i, (t, g, name) in enumerate(((q, dq_out, "q"), (k, dk_out, "k"))):
-        if norm is None and t is None:
-            continue
-        lds[i] = _heads(t, dq_out, name, (dq_out.dtype,))
-        if t.shape != g.shape:
-            raise ValueError(f"{name} {tuple(t.shape)} must have the shape of its output's gradient {tuple(g.shape)}")
-    if dv_out is not None:
-        _heads(dv_out, dq_out, "dv_out", (dq_out.dtype,), dense=True)
-        if dv_out.shape != dk_out.shape:
-            raise ValueError("dk_out and dv_out must have the same shape")
-    grads = (dq_out, dk_out, dv_out)
+    outs = None if out is None else tuple(_meta(o) for o in out)
+    plan = _rope_bwd_plan(_meta(dq_out), _meta(dk_out), _meta(dv_out), _meta(q), _meta(k), _meta(q_weight),
+                          _meta(k_weight), _meta(table), outs, tuple(axes), layout, norm, eps)
+    dev = dq_out.device
     if out is None:
-        out = tuple(None if g is None else torch.empty_like(g) for g in grads)
+        dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
+        dv = None if dv_out is None else torch.empty_like(dv_out)
     else:
-        out = tuple(out)
-        for i, (o, g) in enumerate(zip(out, grads)):
-            if (o is None) != (g is None):
-                raise ValueError("out must give dv exactly when dv_out is given")
-            if o is not None:
-                lds[3 + i] = _heads(o, dq_out, "a gradient", (dq_out.dtype,))
-                if o.shape != g.shape:
-                    raise ValueError(f"a gradient must have shape {tuple(g.shape)}, got {tuple(o.shape)}")
-    w_dtype = _weights(dq_out, dk_out, q_weight, k_weight, norm)
-    prm = _rope_params(dq_out, dk_out, axes, layout, norm, eps, dq_out.dtype, (0.0, 0.0, 0.0), lds, w_dtype)
-    table = _check_table(table, dq_out, prm)
-    lib = _lib.load()
+        dq, dk, dv = out
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
+    ws = None
     if dqw is not None or dkw is not None:
-        workspace = _workspace(dq_out, _size(dq_out, lib.basa_qkv_rope_bwd_workspace_size, prm), workspace)
-    else:
-        workspace = None
-    _on(dq_out, lib.basa_qkv_rope_bwd, "basa_qkv_rope_bwd", _p(dq_out), _p(dk_out), _p(dv_out),
-        _p(q) if norm is not None else None, _p(k) if norm is not None else None, _p(q_weight), _p(k_weight),
-        _p(table), _p(out[0]), _p(out[1]), _p(out[2]), _p(dqw), _p(dkw), _p(workspace), ctypes.byref(prm))
-    return (*out, dqw, dkw)
+        ws = _workspace(dev, _size(dev, "basa_qkv_rope_bwd_workspace_size", plan), workspace)
+    _on(dev, _lib.load().basa_qkv_rope_bwd, "basa_qkv_rope_bwd", dq_out.data_ptr(), dk_out.data_ptr(), _p(dv_out),
+        None if norm is None else q.data_ptr(), None if norm is None else k.data_ptr(), _p(q_weight), _p(k_weight),
+        table.data_ptr() if plan.turns else None, dq.data_ptr(), dk.data_ptr(), _p(dv), _p(dqw), _p(dkw), _p(ws),
+        plan.params)
+    return dq, dk, dv, dqw, dkw
 
 
 # ---------------------------------------------------------------------------
@@ -302,34 +374,32 @@ class GatedNormGrads(NamedTuple):
     dshift: Optional[torch.Tensor]
 
 
-def _rows(t, ref, name, dtypes, shape=None):
-    _tensor(t, ref, name, dtypes)
-    if not t.is_contiguous():
+def _rows(m, ref, name, dtypes, shape=None):
+    _tensor(m, ref, name, dtypes)
+    if not _dense(m):
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape is not None and m[0] != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(m[0])}")
 
 
 def _modulation(m, x, name):
     """(rows of a modulation, elements from one to the next; 0: one for all)."""
     _tensor(m, x, name, _FLOAT)
-    C = x.shape[-1]
-    lead = m.shape[:-1]
-    if m.dim() < 1 or m.shape[-1] != C or (C > 1 and m.stride(-1) != 1):
-        raise ValueError(f"{name} must end in {C} dense columns, got {tuple(m.shape)}")
+    shape, stride, xs = m[0], m[1], x[0]
+    C = xs[-1]
+    lead = tuple(shape[:-1])
+    if len(shape) < 1 or shape[-1] != C or (C > 1 and stride[-1] != 1):
+        raise ValueError(f"{name} must end in {C} dense columns, got {tuple(shape)}")
     n = len(lead)
-    if n and tuple(lead) != tuple(x.shape[:n]) and not (
-            n == 2 and x.dim() == 3 and lead[0] == x.shape[0] and lead[1] and x.shape[1] % lead[1] == 0):
-        raise ValueError(f"{name} {tuple(m.shape)} must be [C], or lead with dims of x {tuple(x.shape)}")
-    groups = 1
-    for s in lead:
-        groups *= s
-    return groups, _row_stride(m.shape, m.stride(), n, name) or 0
+    if n and lead != tuple(xs[:n]) and not (
+            n == 2 and len(xs) == 3 and lead[0] == xs[0] and lead[1] and xs[1] % lead[1] == 0):
+        raise ValueError(f"{name} {tuple(shape)} must be [C], or lead with dims of x {tuple(xs)}")
+    return _numel(lead), _row_stride(shape, stride, n, name) or 0
 
 
 def _gnorm_params(x, y_dtype, mods, weights, norm, post_norm, eps, post_eps, res_scale) -> BasaGnormParams:
     """mods: (gate, scale, shift); weights: (post_weight, weight, bias)."""
-    C = x.shape[-1]
+    C = x[0][-1]
     groups, lds, mod_dtype, w_dtype = None, [], None, None
     for m, name in zip(mods, ("gate", "scale", "shift")):
         if m is None:
@@ -338,26 +408,51 @@ def _gnorm_params(x, y_dtype, mods, weights, norm, post_norm, eps, post_eps, res
         g, ld = _modulation(m, x, name)
         if groups not in (None, g):
             raise ValueError("gate, scale and shift must have the same leading dims (expand the shorter)")
-        if mod_dtype not in (None, m.dtype):
+        if mod_dtype not in (None, m[2]):
             raise TypeError("gate, scale and shift must share a dtype")
-        groups, mod_dtype = g, m.dtype
+        groups, mod_dtype = g, m[2]
         lds.append(ld)
     for w, name in zip(weights, ("post_weight", "weight", "bias")):
         if w is None:
             continue
         _rows(w, x, name, _FLOAT)
-        if w.numel() != C:
-            raise ValueError(f"{name} must be {C} values, got {tuple(w.shape)}")
-        if w_dtype not in (None, w.dtype):
+        if _numel(w[0]) != C:
+            raise ValueError(f"{name} must be {C} values, got {tuple(w[0])}")
+        if w_dtype not in (None, w[2]):
             raise TypeError("weight, bias and post_weight must share a dtype")
-        w_dtype = w.dtype
-    rows = 1
-    for s in x.shape[:-1]:
-        rows *= s
-    return BasaGnormParams(rows, max(groups or 1, 1), C, _code(BASA_NORM, norm, "norm"),
+        w_dtype = w[2]
+    return BasaGnormParams(_numel(x[0][:-1]), max(groups or 1, 1), C, _code(BASA_NORM, norm, "norm"),
                            _code(BASA_NORM, post_norm, "post_norm"), float(eps), float(post_eps), float(res_scale),
-                           _DT[x.dtype], _DT[y_dtype], _DT[mod_dtype or torch.float32],
+                           _DT[x[2]], _DT[y_dtype], _DT[mod_dtype or torch.float32],
                            _DT[w_dtype or torch.float32], *lds)
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _gnorm_plan(x, y, mods, weights, x_out, h_out, norm, post_norm, eps, post_eps, res_scale, h_dtype):
+    _rows(x, None, "x", _FLOAT)
+    if len(x[0]) < 2:
+        raise ValueError(f"x must be [..., C], got {tuple(x[0])}")
+    if y is not None:
+        _rows(y, x, "y", _FLOAT, x[0])
+        if h_dtype not in (None, y[2]):
+            raise TypeError(f"h has y's dtype {y[2]}")
+        dt = y[2]
+    else:
+        if mods[0] is not None or post_norm is not None or x_out is not None or norm is None:
+            raise ValueError("without y there is no gate, post_norm or x_out, and norm must be given")
+        if res_scale != 1.0:
+            raise ValueError("res_scale needs y")
+        dt = h_dtype or x[2]
+        if dt not in _FLOAT:
+            raise TypeError(f"h_dtype must be {' or '.join(map(str, _FLOAT))}, got {dt}")
+    if norm is None and h_out is not None:
+        raise ValueError("h_out needs a norm")
+    prm = _gnorm_params(x, dt, mods, weights, norm, post_norm, eps, post_eps, res_scale)
+    if x_out is not None:
+        _rows(x_out, x, "x_out", (x[2],), x[0])
+    if h_out is not None:
+        _rows(h_out, x, "h_out", (dt,), x[0])
+    return _Plan(prm, dtype=dt, stats=(*x[0][:-1], 4))
 
 
 def gated_norm(x, y=None, *, gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None,
@@ -382,39 +477,60 @@ def gated_norm(x, y=None, *, gate=None, post_weight=None, weight=None, bias=None
                               shift=shift, norm=norm, post_norm=post_norm, eps=eps, post_eps=post_eps,
                               res_scale=res_scale, h_dtype=h_dtype, return_stats=return_stats, x_out=x_out,
                               h_out=h_out)
-    _rows(x, None, "x", _FLOAT)
-    if x.dim() < 2:
-        raise ValueError(f"x must be [..., C], got {tuple(x.shape)}")
-    if y is not None:
-        _rows(y, x, "y", _FLOAT, x.shape)
-        if h_dtype not in (None, y.dtype):
-            raise TypeError(f"h has y's dtype {y.dtype}")
-        dt = y.dtype
-    else:
-        if gate is not None or post_norm is not None or x_out is not None or norm is None:
-            raise ValueError("without y there is no gate, post_norm or x_out, and norm must be given")
-        if res_scale != 1.0:
-            raise ValueError("res_scale needs y")
-        dt = h_dtype or x.dtype
-        if dt not in _FLOAT:
-            raise TypeError(f"h_dtype must be {' or '.join(map(str, _FLOAT))}, got {dt}")
-    if norm is None and h_out is not None:
-        raise ValueError("h_out needs a norm")
-    prm = _gnorm_params(x, dt, (gate, scale, shift), (post_weight, weight, bias), norm, post_norm, eps, post_eps,
-                        res_scale)
-    if x_out is not None:
-        _rows(x_out, x, "x_out", (x.dtype,), x.shape)
-    elif y is not None:
+    plan = _gnorm_plan(_meta(x), _meta(y), (_meta(gate), _meta(scale), _meta(shift)),
+                       (_meta(post_weight), _meta(weight), _meta(bias)), _meta(x_out), _meta(h_out), norm, post_norm,
+                       eps, post_eps, res_scale, h_dtype)
+    dev = x.device
+    if x_out is None and y is not None:
         x_out = torch.empty_like(x)
-    if h_out is not None:
-        _rows(h_out, x, "h_out", (dt,), x.shape)
-    elif norm is not None:
-        h_out = torch.empty(x.shape, dtype=dt, device=x.device)
-    stats = torch.empty((*x.shape[:-1], 4), dtype=torch.float32, device=x.device) if return_stats else None
-    _on(x, _lib.load().basa_gated_norm, "basa_gated_norm", _p(x), _p(y), _p(gate), _p(post_weight), _p(weight),
-        _p(bias), _p(scale), _p(shift), _p(x_out), _p(h_out), _p(stats), ctypes.byref(prm))
-    x_out = x if y is None else x_out
+    if h_out is None and norm is not None:
+        h_out = torch.empty(x.shape, dtype=plan.dtype, device=dev)
+    stats = torch.empty(plan.stats, dtype=torch.float32, device=dev) if return_stats else None
+    _on(dev, _lib.load().basa_gated_norm, "basa_gated_norm", x.data_ptr(), _p(y), _p(gate), _p(post_weight),
+        _p(weight), _p(bias), _p(scale), _p(shift), _p(x_out), _p(h_out), _p(stats), plan.params)
+    if y is None:
+        x_out = x
     return (x_out, h_out, stats) if return_stats else (x_out, h_out)
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _gnorm_bwd_plan(dh, x_out, stats, y, dx_out, mods, weights, norm, post_norm, res_scale):
+    ref = x_out if x_out is not None else dx_out
+    _rows(ref, None, "x_out" if x_out is not None else "dx_out", _FLOAT)
+    if len(ref[0]) < 2:
+        raise ValueError(f"x_out must be [..., C], got {tuple(ref[0])}")
+    if (dh is None) != (norm is None):
+        raise ValueError("dh goes with a norm")
+    if norm is not None and x_out is None:
+        raise ValueError("x_out is needed with a norm")
+    if norm is None and dx_out is None:
+        raise ValueError("dx_out is needed without a norm")
+    if y is None and (mods[0] is not None or post_norm is not None or norm is None):
+        raise ValueError("without y there is no gate or post_norm, and norm must be given")
+    if y is None and res_scale != 1.0:
+        raise ValueError("res_scale needs y")
+    dt = dh[2] if dh is not None else y[2]
+    if dh is not None:
+        _rows(dh, ref, "dh", _FLOAT, ref[0])
+    if y is not None:
+        _rows(y, ref, "y", (dt,), ref[0])
+    if dx_out is not None:
+        _rows(dx_out, ref, "dx_out", (ref[2],), ref[0])
+    use_stats = norm is not None or post_norm is not None
+    if use_stats:
+        _rows(stats, ref, "stats", (torch.float32,), torch.Size((*ref[0][:-1], 4)))
+    prm = _gnorm_params(ref, dt, mods, weights, norm, post_norm, 1.0, 1.0, res_scale)
+    return _Plan(prm, use_stats=use_stats, use_y=mods[0] is not None or post_norm is not None)
+
+
+def _grads_like(ts):
+    """Gradients beside tensors of one type; those of one shape in one allocation."""
+    given = [t for t in ts if t is not None]
+    if len(given) > 1 and all(t.shape == given[0].shape for t in given[1:]):
+        t = given[0]
+        parts = iter(torch.empty((len(given), *t.shape), dtype=t.dtype, device=t.device).unbind(0))
+        return [None if t is None else next(parts) for t in ts]
+    return [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ts]
 
 
 def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_weight=None, weight=None, bias=None,
@@ -431,41 +547,21 @@ def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_wei
             return gated_norm_bwd(dh, x_out, stats, y, dx_out, gate=gate, post_weight=post_weight, weight=weight,
                                   bias=bias, scale=scale, shift=shift, norm=norm, post_norm=post_norm,
                                   res_scale=res_scale, workspace=workspace)
+    plan = _gnorm_bwd_plan(_meta(dh), _meta(x_out), _meta(stats), _meta(y), _meta(dx_out),
+                           (_meta(gate), _meta(scale), _meta(shift)),
+                           (_meta(post_weight), _meta(weight), _meta(bias)), norm, post_norm, res_scale)
     ref = x_out if x_out is not None else dx_out
-    _rows(ref, None, "x_out" if x_out is not None else "dx_out", _FLOAT)
-    if ref.dim() < 2:
-        raise ValueError(f"x_out must be [..., C], got {tuple(ref.shape)}")
-    if (dh is None) != (norm is None):
-        raise ValueError("dh goes with a norm")
-    if norm is not None and x_out is None:
-        raise ValueError("x_out is needed with a norm")
-    if norm is None and dx_out is None:
-        raise ValueError("dx_out is needed without a norm")
-    if y is None and (gate is not None or post_norm is not None or norm is None):
-        raise ValueError("without y there is no gate or post_norm, and norm must be given")
-    if y is None and res_scale != 1.0:
-        raise ValueError("res_scale needs y")
-    dt = dh.dtype if dh is not None else y.dtype
-    if dh is not None:
-        _rows(dh, ref, "dh", _FLOAT, ref.shape)
-    if y is not None:
-        _rows(y, ref, "y", (dt,), ref.shape)
-    if dx_out is not None:
-        _rows(dx_out, ref, "dx_out", (ref.dtype,), ref.shape)
-    if norm is not None or post_norm is not None:
-        _rows(stats, ref, "stats", (torch.float32,), torch.Size((*ref.shape[:-1], 4)))
-    prm = _gnorm_params(ref, dt, (gate, scale, shift), (post_weight, weight, bias), norm, post_norm, 1.0, 1.0,
-                        res_scale)
-    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
-    g = GatedNormGrads(torch.empty_like(ref), like(y), like(gate), like(post_weight), like(weight), like(bias),
-                       like(scale), like(shift))
-    lib = _lib.load()
-    if any(t is not None for t in g[2:]):
-        workspace = _workspace(ref, _size(ref, lib.basa_gated_norm_bwd_workspace_size, prm), workspace)
-    else:
-        workspace = None
-    _on(ref, lib.basa_gated_norm_bwd, "basa_gated_norm_bwd", _p(dh), _p(x_out) if norm is not None else None,
-        _p(stats) if norm is not None or post_norm is not None else None,
-        _p(y) if gate is not None or post_norm is not None else None, _p(dx_out), _p(gate), _p(post_weight),
-        _p(weight), _p(bias), _p(scale), *(_p(t) for t in g), _p(workspace), ctypes.byref(prm))
-    return g
+    dev = ref.device
+    dx = torch.empty_like(ref)
+    dy = None if y is None else torch.empty_like(y)
+    dgate, dscale, dshift = _grads_like((gate, scale, shift))
+    dpw, dw, db = _grads_like((post_weight, weight, bias))
+    ws = None
+    if dgate is not None or dscale is not None or dshift is not None or dpw is not None or dw is not None \
+            or db is not None:
+        ws = _workspace(dev, _size(dev, "basa_gated_norm_bwd_workspace_size", plan), workspace)
+    _on(dev, _lib.load().basa_gated_norm_bwd, "basa_gated_norm_bwd", _p(dh), _p(x_out) if norm is not None else None,
+        _p(stats) if plan.use_stats else None, _p(y) if plan.use_y else None, _p(dx_out), _p(gate), _p(post_weight),
+        _p(weight), _p(bias), _p(scale), dx.data_ptr(), _p(dy), _p(dgate), _p(dpw), _p(dw), _p(db), _p(dscale),
+        _p(dshift), _p(ws), plan.params)
+    return GatedNormGrads(dx, dy, dgate, dpw, dw, db, dscale, dshift)
