@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         flushed = true;
       }
       if (r == r1) break;
+      if (r1 - r <= a.group) dependents_may_start();
       g = r / a.group;
       end = (int)min((long long)r1, (g + 1) * a.group);
 #pragma unroll
@@ -804,6 +805,7 @@ struct GnJoin {
 };
 __global__ void __launch_bounds__(256) gnorm_join_kernel(GnJoin a) {
   __shared__ float red[3][32][9];
+  wait_for_partial_sums();
   const int k = threadIdx.x & 7, lane = threadIdx.x >> 3;
   const int c = blockIdx.x * 8 + k;
   float v[3] = {0.f, 0.f, 0.f};
@@ -820,14 +822,18 @@ __global__ void __launch_bounds__(256) gnorm_join_kernel(GnJoin a) {
     const long long lo = ((g * a.group + 1) * a.grid - 1) / a.rows;
     const long long hi = ((g + 1) * a.group * a.grid - 1) / a.rows;
     if (lo == hi) return;  // inside one CTA, which has written the result
-    for (long long i = lo + lane; i <= hi; i += 32) {
-      const bool first = a.rows * i / a.grid / a.group == g;
-      const float* p = a.part_g + (i * 2 + !first) * 3 * a.C + c;
+    // a CTA behind the first one begins inside this row of modulations, so its
+    // sums are the CTA's first; in the first one they may be its last
+    const bool whole = a.rows * lo / a.grid / a.group == g;
+#pragma unroll 4
+    for (int i = (int)lo + lane; i <= (int)hi; i += 32) {
+      const float* p = a.part_g + (i * 2 + (i == (int)lo && !whole ? 1 : 0)) * 3LL * a.C + c;
 #pragma unroll
       for (int s = 0; s < 3; ++s) v[s] += p[s * a.C];
     }
   } else {
     if (blockIdx.y || !a.part_w) return;
+#pragma unroll 4
     for (int i = lane; i < a.grid; i += 32) {
       const float* p = a.part_w + (long long)i * 3 * a.C + c;
 #pragma unroll
@@ -1120,8 +1126,8 @@ basa_status basa_gated_norm_bwd(const void* dh, const void* x_out, const float* 
   j.by_group = p->groups <= sh.grid;
   j.mod_bf16 = a.mod_bf16; j.w_bf16 = a.w_bf16;
   const unsigned gy = !mods ? 1u : (unsigned)(j.by_group ? p->groups : sh.grid);
-  gnorm_join_kernel<<<dim3((unsigned)(p->C / 8), gy, weights ? 2 : 1), 256, 0, stream>>>(j);
-  return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+  return launch_dependent(gnorm_join_kernel, dim3((unsigned)(p->C / 8), gy, weights ? 2 : 1), 256,
+                          stream, j);
 }
 
 }  // extern "C"

@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
     }
   }
   if (kNorm && P.part) {  // uniform over the CTA
+    dependents_may_start();
     float fa[8], fb[8];
     order16<kHalves>(accA, accB, fa, fb);
 #pragma unroll
@@ -542,44 +543,61 @@ struct TokenSmem {
   float4 cs[2][32];  // two pairs' (cos, sin)
 };
 
-__device__ __forceinline__ float2 block_sum(float2 v, TokenSmem& sm, int buf) {
-  v = lane_sum<32>(v);
-  if ((threadIdx.x & 31) == 0) sm.red[buf][threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int i = threadIdx.x & 31;
-  v = i < (int)(blockDim.x >> 5) ? sm.red[buf][i] : make_float2(0.f, 0.f);
-  return lane_sum<32>(v);
+// A part with fewer heads than q needs fewer warps: the others leave at once,
+// and the barrier counts those that stay.
+__device__ __forceinline__ void part_sync(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
-__device__ __forceinline__ float block_sum(float v, TokenSmem& sm, int buf) {
+__device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, int threads) {
+  // the lanes of each half keep one of the two sums and hand on the other
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16;
+  float k = (hi ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, hi ? v.x : v.y, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+  float* red = reinterpret_cast<float*>(sm.red[buf]);
+  if ((lane & 15) == 0) red[2 * (threadIdx.x >> 5) + (lane >> 4)] = k;
+  part_sync(threads);
+  k = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < threads >> 4) k += red[lane + 32 * i];
+#pragma unroll
+  for (int o = 16; o > 1; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+  return make_float2(__shfl_sync(0xffffffffu, k, 0), __shfl_sync(0xffffffffu, k, 1));
+}
+__device__ __forceinline__ float part_sum(float v, TokenSmem& sm, int buf, int threads) {
   v = lane_sum<32>(v);
-  if ((threadIdx.x & 31) == 0) sm.red[buf][threadIdx.x >> 5].x = v;
-  __syncthreads();
-  const int i = threadIdx.x & 31;
-  return lane_sum<32>(i < (int)(blockDim.x >> 5) ? sm.red[buf][i].x : 0.f);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sm.red[buf][threadIdx.x >> 5].x = v;
+  part_sync(threads);
+  return lane_sum<32>(lane < threads >> 5 ? sm.red[buf][lane].x : 0.f);
 }
 
 // A thread's weights in shared memory: eight 16-byte pieces for each of its kV
 // groups of sixteen, the threads side by side.
-__device__ __forceinline__ void put_weights(char* at, int j, const f2 (&A)[4], const f2 (&B)[4]) {
-  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + (size_t)j * 4 * blockDim.x + threadIdx.x;
+__device__ __forceinline__ void put_weights(char* at, int j, int threads, const f2 (&A)[4],
+                                            const f2 (&B)[4]) {
+  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + j * 4 * threads + threadIdx.x;
   w[0] = make_ulonglong2(A[0], A[1]);
-  w[blockDim.x] = make_ulonglong2(A[2], A[3]);
-  w[2 * blockDim.x] = make_ulonglong2(B[0], B[1]);
-  w[3 * blockDim.x] = make_ulonglong2(B[2], B[3]);
+  w[threads] = make_ulonglong2(A[2], A[3]);
+  w[2 * threads] = make_ulonglong2(B[0], B[1]);
+  w[3 * threads] = make_ulonglong2(B[2], B[3]);
 }
-__device__ __forceinline__ void get_weights(const char* at, int j, f2 (&A)[4], f2 (&B)[4]) {
+__device__ __forceinline__ void get_weights(const char* at, int j, int threads, f2 (&A)[4],
+                                            f2 (&B)[4]) {
   const ulonglong2* w =
-      reinterpret_cast<const ulonglong2*>(at) + (size_t)j * 4 * blockDim.x + threadIdx.x;
+      reinterpret_cast<const ulonglong2*>(at) + j * 4 * threads + threadIdx.x;
   ulonglong2 v = w[0];
   A[0] = v.x;
   A[1] = v.y;
-  v = w[blockDim.x];
+  v = w[threads];
   A[2] = v.x;
   A[3] = v.y;
-  v = w[2 * blockDim.x];
+  v = w[2 * threads];
   B[0] = v.x;
   B[1] = v.y;
-  v = w[3 * blockDim.x];
+  v = w[3 * threads];
   B[2] = v.x;
   B[3] = v.y;
 }
@@ -592,7 +610,9 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
   constexpr int kDepth = kStages<TI>;
   const int part = blockIdx.y;
   const RopePart P = pick(a, part);
-  const int lph = a.d / 16, units = P.heads * lph, tid = threadIdx.x, threads = blockDim.x;
+  const int lph = a.d / 16, units = P.heads * lph, tid = threadIdx.x;
+  const int threads = min((int)blockDim.x, (units + 32 * kV - 1) / (32 * kV) * 32);
+  if (tid >= threads) return;
   const float inv = 1.f / (float)(P.heads * a.d);
   const Lane l = lane_of<kHalves>(a, tid % lph);
   const int h0 = tid / lph * a.d, dh = threads / lph * a.d;  // a thread's heads, in elements
@@ -660,7 +680,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
   for (int j = 0; j < kV; ++j) {
     f2 A[4], B[4];
     weight16<kHalves>(on[j] ? P.w : nullptr, a.w_bf16, h0 + j * dh, l, A, B);
-    put_weights(weights, j, A, B);
+    put_weights(weights, j, threads, A, B);
   }
   int buf = 0;
   for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
       for (int i = 0; i < 4; ++i) s = fma2(B[j][i], B[j][i], fma2(A[j][i], A[j][i], s));
     }
     from = from + stage == kDepth * stage ? 0 : from + stage;
-    const float r = mul * rsqrtf(block_sum(sum2(s), sm, buf) * inv + a.eps);
+    const float r = mul * rsqrtf(part_sum(sum2(s), sm, buf, threads) * inv + a.eps);
     const f2 rr = pk(r, r);
     f2 C[4], S[4], N[4];  // N = -S
     angles_of(sm.cs[buf], l, C, S);
@@ -689,7 +709,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       f2 WA[4], WB[4];
-      get_weights(weights, j, WA, WB);
+      get_weights(weights, j, threads, WA, WB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 p = mul2(A[j][i], WA[i]), q = mul2(B[j][i], WB[i]);
@@ -710,7 +730,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
   __shared__ TokenSmem sm;
   const int part = blockIdx.y;
   const RopePart P = pick(a, part);
-  const int lph = a.d / 16, tid = threadIdx.x, threads = blockDim.x;
+  const int lph = a.d / 16, tid = threadIdx.x;
+  const int threads = min((int)blockDim.x, (P.heads * lph + 31) / 32 * 32);
+  if (tid >= threads) return;
   const float inv = 1.f / (float)(P.heads * a.d);
   const Lane l = lane_of<kHalves>(a, tid % lph);
   const bool on = tid < P.heads * lph;
@@ -773,11 +795,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
   {
     f2 A[4], B[4];
     weight16<kHalves>(on ? P.w : nullptr, a.w_bf16, h0, l, A, B);
-    put_weights(weights, 0, A, B);
+    put_weights(weights, 0, threads, A, B);
 #pragma unroll
     for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
   }
-  __syncthreads();
+  part_sync(threads);
   int buf = 0;
   for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
     fetch();
@@ -793,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
         GB[i] = fma2(B[i], C[i], mul2(A[i], neg2(S[i])));
       }
       take(2, XA, XB);
-      get_weights(weights, 0, A, B);
+      get_weights(weights, 0, threads, A, B);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s = fma2(XB[i], XB[i], fma2(XA[i], XA[i], s));
@@ -803,12 +825,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
     from = depth == 2 ? stage - from : 0;
     ang.ahead(a);  // the next token's angles, written ahead of the barrier
     ang.put(sm.cs[buf ^ 1], tid, threads);
-    const float2 t = block_sum(make_float2(sum2(s), sum2(d)), sm, buf);
+    const float2 t = part_sum(make_float2(sum2(s), sum2(d)), sm, buf, threads);
     const float r = rsqrtf(t.x * inv + a.eps);
     const float c = -t.y * inv * r * r * r;
     const f2 rr = pk(r, r), cc = pk(c, c);
     f2 WA[4], WB[4];
-    get_weights(weights, 0, WA, WB);
+    get_weights(weights, 0, threads, WA, WB);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f2 pA = mul2(GA[i], rr), pB = mul2(GB[i], rr);
@@ -819,6 +841,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
     }
     if (on) pack16<kHalves>(o, l, GA, GB);
   }
+  dependents_may_start();
   if (P.part && on)
     pack16<kHalves>(P.part + (long long)blockIdx.x * P.heads * a.d + h0, l, accA, accB);
 }
@@ -833,10 +856,12 @@ struct ColSum {
 };
 __global__ void __launch_bounds__(256) rope_colsum_kernel(ColSum s0, ColSum s1, int bf16) {
   __shared__ float red[32][9];
+  wait_for_partial_sums();
   const ColSum s = blockIdx.y ? s1 : s0;
   const int c = blockIdx.x * 8 + (threadIdx.x & 7), lane = threadIdx.x >> 3;
   if (blockIdx.x * 8 >= s.cols || !s.out) return;  // cols is a multiple of 8
   float v = 0.f;
+#pragma unroll 8
   for (int r = lane; r < s.rows; r += 32) v += s.part[(long long)r * s.cols + c];
   red[lane][threadIdx.x & 7] = v;
   __syncthreads();
@@ -950,7 +975,9 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
     g.chunks[0] = g.chunks[1] = 1;
     g.steps[0] = g.steps[1] = 0;
     g.y = with_v ? 3 : 2;
-    const int per_sm = (bwd ? 640 : 640) / g.threads;
+    // q's and k's CTAs on the SMs at a time (96 and 128 registers a thread); more
+    // would only leave more rows of partial sums
+    const int per_sm = (bwd ? 320 : 640) / g.threads;
     const long long cap = (long long)sms * (per_sm > 1 ? per_sm : 1);
     g.x = (unsigned)(r.tokens < cap ? r.tokens : cap);
     return g;
@@ -1034,6 +1061,9 @@ bool go_bwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cud
     if (g.threads <= 320)
       return halves ? go_token(rope_token_bwd_kernel<T, 320, 2, true>, g, smem, st, a, depth)
                     : go_token(rope_token_bwd_kernel<T, 320, 2, false>, g, smem, st, a, depth);
+    if (g.threads <= 512)
+      return halves ? go_token(rope_token_bwd_kernel<T, 512, 1, true>, g, smem, st, a, depth)
+                    : go_token(rope_token_bwd_kernel<T, 512, 1, false>, g, smem, st, a, depth);
     return halves ? go_token(rope_token_bwd_kernel<T, 1024, 1, true>, g, smem, st, a, depth)
                   : go_token(rope_token_bwd_kernel<T, 1024, 1, false>, g, smem, st, a, depth);
   }
@@ -1200,10 +1230,10 @@ basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void
   if (sums) {
     const ColSum c0{a.q.part, dq_weight, (int)g.x * g.chunks[0], cols[0]};
     const ColSum c1{a.k.part, dk_weight, (int)g.x * g.chunks[1], cols[1]};
-    rope_colsum_kernel<<<dim3((unsigned)(cols[0] / 8), 2), 256, 0, stream>>>(
-        c0, c1, p->w_dtype == BASA_BF16);
+    return launch_dependent(rope_colsum_kernel, dim3((unsigned)(cols[0] / 8), 2), 256, stream, c0,
+                            c1, (int)(p->w_dtype == BASA_BF16));
   }
-  return launched();
+  return BASA_OK;
 }
 
 }  // extern "C"

@@ -234,9 +234,33 @@ __device__ __forceinline__ float2 lane_sum(float2 v) {
   return v;
 }
 
+// Programmatic dependent launch: a kernel that ends a gradient's sums is launched
+// while the one that leaves the partial sums still runs, and waits for it.
+__device__ __forceinline__ void dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_partial_sums() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+template <typename... P, typename... A>
+basa_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+}
+
 inline int row_sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
