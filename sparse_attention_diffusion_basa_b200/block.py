@@ -74,6 +74,11 @@ def _size(device, name, ref) -> int:
         return int(getattr(_lib.load(), name)(ref.params))
 
 
+def _like(t, dtype=None):
+    """A dense tensor of t's shape (half the host time of torch.empty with a shape)."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _workspace(device, need, workspace):
     if not need:
         return None
@@ -288,8 +293,7 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
     dev = q.device
     if out is None:
         dt = plan.dtype
-        qo, ko = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-        vo = None if v is None else torch.empty(k.shape, dtype=dt, device=dev)
+        qo, ko, vo = _like(q, dt), _like(k, dt), None if v is None else _like(v, dt)
     else:
         qo, ko, vo = out
     _on(dev, _lib.load().basa_qkv_rope, "basa_qkv_rope", q.data_ptr(), k.data_ptr(), _p(v), _p(q_weight),
@@ -343,12 +347,11 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
                           _meta(k_weight), _meta(table), outs, tuple(axes), layout, norm, eps)
     dev = dq_out.device
     if out is None:
-        dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
-        dv = None if dv_out is None else torch.empty_like(dv_out)
+        dq, dk, dv = _like(dq_out), _like(dk_out), None if dv_out is None else _like(dv_out)
     else:
         dq, dk, dv = out
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    dqw = None if q_weight is None else _like(q_weight)
+    dkw = None if k_weight is None else _like(k_weight)
     ws = None
     if dqw is not None or dkw is not None:
         ws = _workspace(dev, _size(dev, "basa_qkv_rope_bwd_workspace_size", plan), workspace)
@@ -482,9 +485,9 @@ def gated_norm(x, y=None, *, gate=None, post_weight=None, weight=None, bias=None
                        eps, post_eps, res_scale, h_dtype)
     dev = x.device
     if x_out is None and y is not None:
-        x_out = torch.empty_like(x)
+        x_out = _like(x)
     if h_out is None and norm is not None:
-        h_out = torch.empty(x.shape, dtype=plan.dtype, device=dev)
+        h_out = _like(x, plan.dtype)
     stats = torch.empty(plan.stats, dtype=torch.float32, device=dev) if return_stats else None
     _on(dev, _lib.load().basa_gated_norm, "basa_gated_norm", x.data_ptr(), _p(y), _p(gate), _p(post_weight),
         _p(weight), _p(bias), _p(scale), _p(shift), _p(x_out), _p(h_out), _p(stats), plan.params)
@@ -523,16 +526,6 @@ def _gnorm_bwd_plan(dh, x_out, stats, y, dx_out, mods, weights, norm, post_norm,
     return _Plan(prm, use_stats=use_stats, use_y=mods[0] is not None or post_norm is not None)
 
 
-def _grads_like(ts):
-    """Gradients beside tensors of one type; those of one shape in one allocation."""
-    given = [t for t in ts if t is not None]
-    if len(given) > 1 and all(t.shape == given[0].shape for t in given[1:]):
-        t = given[0]
-        parts = iter(torch.empty((len(given), *t.shape), dtype=t.dtype, device=t.device).unbind(0))
-        return [None if t is None else next(parts) for t in ts]
-    return [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ts]
-
-
 def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_weight=None, weight=None, bias=None,
                    scale=None, shift=None, norm="layer", post_norm=None, res_scale=1.0, workspace=None, stream=None
                    ) -> GatedNormGrads:
@@ -552,10 +545,9 @@ def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_wei
                            (_meta(post_weight), _meta(weight), _meta(bias)), norm, post_norm, res_scale)
     ref = x_out if x_out is not None else dx_out
     dev = ref.device
-    dx = torch.empty_like(ref)
-    dy = None if y is None else torch.empty_like(y)
-    dgate, dscale, dshift = _grads_like((gate, scale, shift))
-    dpw, dw, db = _grads_like((post_weight, weight, bias))
+    dx = _like(ref)
+    dy, dgate, dpw, dw, db, dscale, dshift = (
+        None if t is None else _like(t) for t in (y, gate, post_weight, weight, bias, scale, shift))
     ws = None
     if dgate is not None or dscale is not None or dshift is not None or dpw is not None or dw is not None \
             or db is not None:
