@@ -164,6 +164,14 @@ __device__ __forceinline__ void affine8(const GnArgs& a, long long g, int col, f
     for (int i = 0; i < 4; ++i) B[i] = fma2(b[i], p[i], B[i]);
   }
 }
+__device__ __forceinline__ void params_ahead(const GnArgs& a, long long g, int col) {
+  ahead8(a.gate, a.mod_bf16, g * a.ld_gate + col);
+  ahead8(a.pw, a.w_bf16, col);
+  ahead8(a.scale, a.mod_bf16, g * a.ld_scale + col);
+  ahead8(a.w, a.w_bf16, col);
+  ahead8(a.shift, a.mod_bf16, g * a.ld_shift + col);
+  ahead8(a.b, a.w_bf16, col);
+}
 // An array of fp32 factors in shared memory: two 16-byte pieces of a vector, the
 // first pieces of all vectors and then the second ones, `half` bytes further.
 // One more vector of zeros stands for all vectors past the row's end.
@@ -387,6 +395,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   };
   auto fill = [&](long long g, int v) {
     f2 S[4] = {0, 0, 0, 0}, B[4] = {0, 0, 0, 0};
+    if (v < nvec) params_ahead(a, g, v * 8);
     if (kBranch) {
       if (v < nvec) gate8(a, g, v * 8, S);
       put8(sG + v * 16, half, S);
@@ -500,6 +509,7 @@ __device__ __forceinline__ void flush(const GnArgs& a, const ColSums<kV>& c, lon
     const int col = (j * (int)blockDim.x + (int)threadIdx.x) * 8;
     if (col >= a.C) continue;
     f2 v[4], p[4], q[4];
+    params_ahead(a, g, col);
     if (a.part_w) {
       auto add = [&](float* to, const f2(&sum)[4]) {
         f2 old[4];
@@ -646,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kV; ++j) {  // each thread reads the factors that it writes
         f2 p[4] = {0, 0, 0, 0}, q[4];
+        if (c.ok(j)) params_ahead(a, g, c.col(j));
         if (kBranch) {
           if (c.ok(j)) gate8(a, g, c.col(j), p);
           put8(sG + c.at(j), half, p);

@@ -202,6 +202,13 @@ __device__ __forceinline__ void param8(const void* p, bool bf16, long long col, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
 }
+// Eight parameters on their way to L1, so that those of several kinds that a
+// kernel takes one after another wait for memory once.
+__device__ __forceinline__ void ahead8(const void* p, bool bf16, long long col) {
+  if (p)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(p) +
+                                                  col * (bf16 ? 2 : 4)));
+}
 // Gradients of parameters, in the parameters' type.
 __device__ __forceinline__ void store_param8(void* p, bool bf16, long long col, const f2 (&f)[4]) {
   if (bf16)
