@@ -253,18 +253,6 @@ __device__ __forceinline__ void put_row(float* p, const f2 (&f)[4], bool wide) {
     store8(p, f);
 }
 
-// The same value, but one that the compiler takes for a new one: what is formed
-// from it inside a loop is not moved ahead of the loop, where it would hold
-// registers that the loop does not have.
-__device__ __forceinline__ int anew(int v) {
-  asm volatile("" : "+r"(v));
-  return v;
-}
-
-// Keeps the compiler from loading all of a loop's vectors ahead of using the
-// first, for the same reason.
-__device__ __forceinline__ void one_by_one() { asm volatile("" ::: "memory"); }
-
 // Elements of a row in this warp.
 __device__ __forceinline__ float elements_of(const Team& t, int kv, int nvec) {
   int n = 0;

@@ -25,13 +25,14 @@ struct RopePart {      // one of q, k, v
   float* part;         // backward: partial sums of the weight's gradient
   long long ldx, ldg, ldo;
   int heads;
+  int ctas;            // along the tokens
   int chunks;          // CTAs that share a token's heads
   int steps;           // of 512 / d heads each, per chunk
   float mul;           // e4m3 output: 1 / descale
 };
 
 struct RopeArgs {
-  RopePart q, k, v;
+  RopePart part[3];    // q, k, v; read from the parameter bank where they are used
   const float2* table;
   uint32_t tokens, T, Hg, Wg;
   int nt, nh, nw;      // rotated pairs per axis
@@ -39,10 +40,6 @@ struct RopeArgs {
   float eps;
   int w_bf16;
 };
-
-__device__ __forceinline__ RopePart pick(const RopeArgs& a, int part) {
-  return part == 0 ? a.q : part == 1 ? a.k : a.v;
-}
 
 // A lane holds sixteen elements of a head: two vectors of eight, at ea and eb.
 // They are kept as eight packed pairs A[4], B[4] such that (A[i], B[i]) are the
@@ -200,14 +197,17 @@ __device__ __forceinline__ f2 neg2(f2 v) {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
-// Which of q, k, v a CTA works on, and the chunk of its heads.
-__device__ __forceinline__ int part_of(const RopeArgs& a, int& chunk) {
-  chunk = blockIdx.y;
-  if (chunk < a.q.chunks) return 0;
-  chunk -= a.q.chunks;
-  if (chunk < a.k.chunks) return 1;
-  chunk -= a.k.chunks;
-  return 2;
+// Which of q, k, v a CTA works on, the chunk of its heads, and its number among
+// the CTAs along the tokens.  Each part has CTAs in proportion to its work.
+__device__ __forceinline__ int part_of(const RopeArgs& a, int& chunk, int& cta) {
+  int i = blockIdx.x, part = 0;
+  while (part < 2 && i >= a.part[part].ctas * a.part[part].chunks) {
+    i -= a.part[part].ctas * a.part[part].chunks;
+    ++part;
+  }
+  chunk = i / a.part[part].ctas;
+  cta = i - chunk * a.part[part].ctas;
+  return part;
 }
 
 // v: rows copied (or narrowed) two heads' worth at a time.
@@ -292,20 +292,20 @@ template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
 // across tokens.  The norm's weight is folded into the angles:
 // A' = r (A (wA cos) - B (wB sin)).
 template <typename TI, typename TO, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<TI>;
   constexpr int kStage = Slot<TI>::bytes(2, 32);
   __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
   __shared__ float4 cs[kRopeWarps][2][32];
-  int chunk;
-  const int part = part_of(a, chunk);
-  const RopePart P = pick(a, part);
+  int chunk, cta;
+  const int part = part_of(a, chunk, cta);
+  const RopePart& P = a.part[part];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, slot = lane / kLph;
   const int h0 = chunk * P.steps * kHpw + slot;
   const int hend = min(P.heads, (chunk + 1) * P.steps * kHpw);
-  const uint32_t stride = gridDim.x * kRopeWarps;
+  const uint32_t stride = P.ctas * kRopeWarps;
   const Lane l = lane_of<kHalves>(a, lane % kLph);
-  uint32_t n = blockIdx.x * kRopeWarps + warp;
+  uint32_t n = cta * kRopeWarps + warp;
   const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx;
   TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo;
   const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
@@ -395,21 +395,21 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(RopeArgs a) 
 // in a lane's own sixteen columns over all its tokens and heads, then over the
 // CTA, and left as one row of partial sums a CTA.
 template <typename T, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<T>;
   constexpr int kStage = Slot<T>::bytes(kNorm ? 4 : 2, 32);
   __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
   __shared__ float4 cs[kRopeWarps][2][32];
   __shared__ float red[kRopeWarps][kD];
-  int chunk;
-  const int part = part_of(a, chunk);
-  const RopePart P = pick(a, part);
+  int chunk, cta;
+  const int part = part_of(a, chunk, cta);
+  const RopePart& P = a.part[part];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, slot = lane / kLph;
   const int h0 = chunk * P.steps * kHpw + slot;
   const int hend = min(P.heads, (chunk + 1) * P.steps * kHpw);
-  const uint32_t stride = gridDim.x * kRopeWarps;
+  const uint32_t stride = P.ctas * kRopeWarps;
   const Lane l = lane_of<kHalves>(a, lane % kLph);
-  uint32_t n = blockIdx.x * kRopeWarps + warp;
+  uint32_t n = cta * kRopeWarps + warp;
   const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg;
   T* o = static_cast<T*>(P.o) + (long long)n * P.ldo;
   const long long dg = (long long)stride * P.ldg, dout = (long long)stride * P.ldo;
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < kRopeWarps; ++i) v += red[i][c];
-      P.part[((long long)blockIdx.x * P.chunks + chunk) * kD + c] = v;
+      P.part[((long long)cta * P.chunks + chunk) * kD + c] = v;
     }
   }
 }
@@ -538,17 +538,75 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(RopeArgs
 // behind the barrier that the row's sum needs anyway.  The weights' columns of a
 // thread lie in shared memory too (fp32, read by that thread alone): in
 // registers they would halve the CTAs of an SM.
+constexpr int kCs = 5;  // kStages + 1 of bf16
 struct TokenSmem {
   float2 red[2][32];
-  float4 cs[2][32];  // two pairs' (cos, sin)
+  float4 cs[kCs][32];  // two pairs' (cos, sin), a buffer a token
 };
 
-// A part with fewer heads than q needs fewer warps: the others leave at once,
-// and the barrier counts those that stay.
-__device__ __forceinline__ void part_sync(int threads) {
-  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-}
-__device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, int threads) {
+// A token's angles on their way to shared memory, a thread's two pairs, as part
+// of the thread's next group of copies: forward, of the token whose row the group
+// brings (kDepth - 1 ahead), read behind that token's barrier; backward, of the
+// token after the next, read ahead of its own barrier and behind the one before,
+// by which every thread has waited for its copies.  Either way a buffer is
+// written anew only when the barrier of the token behind its last reader's has
+// been passed: kDepth + 1 buffers forward, 3 backward.  Pairs that are not
+// rotated are (1, 0) in every buffer from the start.
+struct TokenAngles {
+  Coord at;
+  int spot[2];  // base of the pair in the table, axis in the two highest bits
+  __device__ __forceinline__ void init(const RopeArgs& a, uint32_t n, uint32_t step, int tid,
+                                       int threads, TokenSmem& sm) {
+    at.init(a, n, step);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = tid + i * threads;
+      const Spot s = spot_of(a, j < 64 ? j : -1);
+      spot[i] = s.base | s.axis << 30;
+      if (s.axis == 3 && j < 64) {
+#pragma unroll
+        for (int b = 0; b < kCs; ++b)
+          reinterpret_cast<float2*>(sm.cs[b])[j] = make_float2(1.f, 0.f);
+      }
+    }
+  }
+  // Of the coordinates' token, which then move on to the next.
+  __device__ __forceinline__ void fetch(const RopeArgs& a, TokenSmem& sm, int buf, int tid,
+                                        int threads) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t axis = (uint32_t)spot[i] >> 30;
+      if (axis != 3u) {
+        const int off = axis == 0u ? (int)at.t * a.nt : axis == 1u ? (int)at.y * a.nh
+                                                                   : (int)at.x * a.nw;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                         shared_u32(sm.cs[buf]) + (tid + i * threads) * 8),
+                     "l"(a.table + (spot[i] & 0x3fffffff) + off)
+                     : "memory");
+      }
+    }
+    at.next(a);
+  }
+};
+__device__ __forceinline__ int after(int cs) { return cs == kCs - 1 ? 0 : cs + 1; }
+
+// A part with fewer heads than q needs fewer warps a token: a CTA then takes
+// several tokens side by side, a team of warps each.
+constexpr int kMaxTeams = 8;
+static_assert(sizeof(TokenSmem) % 128 == 0, "stages begin at 128 bytes");
+struct TokenTeam {
+  int threads, id, count, tid;  // of a team, this team, teams of the CTA, thread of the team
+  __device__ __forceinline__ TokenTeam(int units, int per_thread) {
+    threads = min((int)blockDim.x, (units + 32 * per_thread - 1) / (32 * per_thread) * 32);
+    count = min((int)blockDim.x / threads, kMaxTeams);
+    id = threadIdx.x / threads;
+    tid = threadIdx.x - id * threads;
+  }
+  __device__ __forceinline__ void sync() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+  }
+};
+__device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, const TokenTeam& t) {
   // the lanes of each half keep one of the two sums and hand on the other
   const int lane = threadIdx.x & 31;
   const bool hi = lane & 16;
@@ -556,81 +614,78 @@ __device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, int
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
   float* red = reinterpret_cast<float*>(sm.red[buf]);
-  if ((lane & 15) == 0) red[2 * (threadIdx.x >> 5) + (lane >> 4)] = k;
-  part_sync(threads);
+  if ((lane & 15) == 0) red[2 * (t.tid >> 5) + (lane >> 4)] = k;
+  t.sync();
   k = 0.f;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (lane + 32 * i < threads >> 4) k += red[lane + 32 * i];
+    if (lane + 32 * i < t.threads >> 4) k += red[lane + 32 * i];
 #pragma unroll
   for (int o = 16; o > 1; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
   return make_float2(__shfl_sync(0xffffffffu, k, 0), __shfl_sync(0xffffffffu, k, 1));
 }
-__device__ __forceinline__ float part_sum(float v, TokenSmem& sm, int buf, int threads) {
+__device__ __forceinline__ float part_sum(float v, TokenSmem& sm, int buf, const TokenTeam& t) {
   v = lane_sum<32>(v);
   const int lane = threadIdx.x & 31;
-  if (lane == 0) sm.red[buf][threadIdx.x >> 5].x = v;
-  part_sync(threads);
-  return lane_sum<32>(lane < threads >> 5 ? sm.red[buf][lane].x : 0.f);
+  if (lane == 0) sm.red[buf][t.tid >> 5].x = v;
+  t.sync();
+  return lane_sum<32>(lane < t.threads >> 5 ? sm.red[buf][lane].x : 0.f);
 }
 
 // A thread's weights in shared memory: eight 16-byte pieces for each of its kV
-// groups of sixteen, the threads side by side.
-__device__ __forceinline__ void put_weights(char* at, int j, int threads, const f2 (&A)[4],
+// groups of sixteen (A's, then B's), the team's threads side by side.
+__device__ __forceinline__ void put_weights(char* at, int j, const TokenTeam& t, const f2 (&A)[4],
                                             const f2 (&B)[4]) {
-  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + j * 4 * threads + threadIdx.x;
+  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + j * 4 * t.threads + t.tid;
   w[0] = make_ulonglong2(A[0], A[1]);
-  w[threads] = make_ulonglong2(A[2], A[3]);
-  w[2 * threads] = make_ulonglong2(B[0], B[1]);
-  w[3 * threads] = make_ulonglong2(B[2], B[3]);
+  w[t.threads] = make_ulonglong2(A[2], A[3]);
+  w[2 * t.threads] = make_ulonglong2(B[0], B[1]);
+  w[3 * t.threads] = make_ulonglong2(B[2], B[3]);
 }
-__device__ __forceinline__ void get_weights(const char* at, int j, int threads, f2 (&A)[4],
-                                            f2 (&B)[4]) {
+// Group j's A (second = 0) or B (1).
+__device__ __forceinline__ void get_weights(const char* at, int j, int second, const TokenTeam& t,
+                                            f2 (&W)[4]) {
   const ulonglong2* w =
-      reinterpret_cast<const ulonglong2*>(at) + j * 4 * threads + threadIdx.x;
+      reinterpret_cast<const ulonglong2*>(at) + (j * 4 + 2 * second) * t.threads + t.tid;
   ulonglong2 v = w[0];
-  A[0] = v.x;
-  A[1] = v.y;
-  v = w[threads];
-  A[2] = v.x;
-  A[3] = v.y;
-  v = w[2 * threads];
-  B[0] = v.x;
-  B[1] = v.y;
-  v = w[3 * threads];
-  B[2] = v.x;
-  B[3] = v.y;
+  W[0] = v.x;
+  W[1] = v.y;
+  v = w[t.threads];
+  W[2] = v.x;
+  W[3] = v.y;
 }
 __host__ __device__ constexpr int weight_bytes(int kv, int threads) { return kv * threads * 64; }
 
 template <typename TI, typename TO, int kV, bool kHalves>
-__global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
-  extern __shared__ __align__(16) char dyn[];
-  __shared__ TokenSmem sm;
+__global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(128) char dyn[];
   constexpr int kDepth = kStages<TI>;
-  const int part = blockIdx.y;
-  const RopePart P = pick(a, part);
-  const int lph = a.d / 16, units = P.heads * lph, tid = threadIdx.x;
-  const int threads = min((int)blockDim.x, (units + 32 * kV - 1) / (32 * kV) * 32);
-  if (tid >= threads) return;
+  int chunk, cta;
+  const int part = part_of(a, chunk, cta);
+  const RopePart& P = a.part[part];
+  const int lph = a.d / 16, units = P.heads * lph;
+  const TokenTeam team(units, kV);
+  if (team.id >= team.count) return;
+  const int tid = team.tid, threads = team.threads;
+  TokenSmem& sm = reinterpret_cast<TokenSmem*>(dyn)[team.id];
   const float inv = 1.f / (float)(P.heads * a.d);
   const Lane l = lane_of<kHalves>(a, tid % lph);
   const int h0 = tid / lph * a.d, dh = threads / lph * a.d;  // a thread's heads, in elements
-  const uint32_t stride = gridDim.x;
-  uint32_t n = blockIdx.x, fn = n;
-  const TI* x = static_cast<const TI*>(P.x) + (long long)n * P.ldx;
-  TO* o = static_cast<TO*>(P.o) + (long long)n * P.ldo + h0;
-  const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
+  const uint32_t stride = P.ctas * team.count;
+  uint32_t n = cta * team.count + team.id, fn = n;
+  if (n >= a.tokens) return;  // a whole team
   bool on[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) on[j] = j * threads + tid < units;
-  char* weights = dyn;
-  char* ring = dyn + weight_bytes(kV, threads);
   const int stage = Slot<TI>::bytes(2 * kV, threads);
+  char* weights = dyn + team.count * (int)sizeof(TokenSmem) +
+                  team.id * (weight_bytes(kV, threads) + kDepth * stage);
+  char* ring = weights + weight_bytes(kV, threads);
   const uint32_t ring_at = shared_u32(ring);
   int to = 0, from = 0;
   auto fetch = [&]() {
     if (fn < a.tokens) {
+      const TI* x = static_cast<const TI*>(P.x) + (uint64_t)fn * (uint32_t)P.ldx;
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
         const TI* head = x + (on[j] ? h0 + j * dh : 0);
@@ -638,7 +693,6 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
         Slot<TI>::fetch(ring_at + to, head + l.eb, 2 * j + 1, threads, tid, on[j]);
       }
       fn += stride;
-      x += dx;
     }
     copy_commit();
     to = to + stage == kDepth * stage ? 0 : to + stage;
@@ -649,12 +703,13 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
     Slot<TI>::take(ring + from, 2 * j + 1, threads, tid, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
-#pragma unroll
-  for (int s = 0; s < kDepth - 1; ++s) fetch();
   const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
   if (part == 2) {
     const f2 mm = pk(mul, mul);
-    for (; n < a.tokens; n += stride, o += dout) {
+#pragma unroll
+    for (int s = 0; s < kDepth - 1; ++s) fetch();
+    for (; n < a.tokens; n += stride) {
+      TO* o = static_cast<TO*>(P.o) + (uint64_t)n * (uint32_t)P.ldo + h0;
       fetch();
       copy_wait<kDepth - 1>();
 #pragma unroll
@@ -674,20 +729,24 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
     }
     return;
   }
-  Gather ang;
-  ang.init(a, n, stride, tid, threads);
+  TokenAngles ang;
+  ang.init(a, n, stride, tid, threads, sm);
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) {
+    ang.fetch(a, sm, s, tid, threads);
+    fetch();
+  }
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     f2 A[4], B[4];
     weight16<kHalves>(on[j] ? P.w : nullptr, a.w_bf16, h0 + j * dh, l, A, B);
-    put_weights(weights, j, threads, A, B);
+    put_weights(weights, j, team, A, B);
   }
-  int buf = 0;
-  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
-    ang.put(sm.cs[buf], tid, threads);
-    ang.ahead(a);
+  int buf = 0, cs = 0, cs_to = kDepth - 1;
+  for (; n < a.tokens; n += stride, buf ^= 1, cs = after(cs), cs_to = after(cs_to)) {
+    copy_wait<kDepth - 2>();  // this token's row and angles
+    ang.fetch(a, sm, cs_to, tid, threads);
     fetch();
-    copy_wait<kDepth - 1>();
     f2 A[kV][4], B[kV][4], s = pk(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
@@ -696,20 +755,22 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
       for (int i = 0; i < 4; ++i) s = fma2(B[j][i], B[j][i], fma2(A[j][i], A[j][i], s));
     }
     from = from + stage == kDepth * stage ? 0 : from + stage;
-    const float r = mul * rsqrtf(part_sum(sum2(s), sm, buf, threads) * inv + a.eps);
+    const float r = mul * rsqrtf(part_sum(sum2(s), sm, buf, team) * inv + a.eps);
     const f2 rr = pk(r, r);
     f2 C[4], S[4], N[4];  // N = -S
-    angles_of(sm.cs[buf], l, C, S);
+    angles_of(sm.cs[cs], l, C, S);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       C[i] = mul2(C[i], rr);
       N[i] = mul2(S[i], pk(-r, -r));
       S[i] = mul2(S[i], rr);
     }
+    TO* o = static_cast<TO*>(P.o) + (uint64_t)n * (uint32_t)P.ldo + h0;
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       f2 WA[4], WB[4];
-      get_weights(weights, j, threads, WA, WB);
+      get_weights(weights, j, 0, team, WA);
+      get_weights(weights, j, 1, team, WB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 p = mul2(A[j][i], WA[i]), q = mul2(B[j][i], WB[i]);
@@ -725,42 +786,41 @@ __global__ void __launch_bounds__(512) rope_token_kernel(RopeArgs a) {
 // barrier; a thread's columns of the weight's gradient stay in registers over
 // all its tokens and are left as one row of partial sums a CTA.
 template <typename T, int kThreads, int kCtas, bool kHalves>
-__global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArgs a, int depth) {
-  extern __shared__ __align__(16) char dyn[];
-  __shared__ TokenSmem sm;
-  const int part = blockIdx.y;
-  const RopePart P = pick(a, part);
-  const int lph = a.d / 16, tid = threadIdx.x;
-  const int threads = min((int)blockDim.x, (P.heads * lph + 31) / 32 * 32);
-  if (tid >= threads) return;
-  const float inv = 1.f / (float)(P.heads * a.d);
+__global__ void __launch_bounds__(kThreads, kCtas)
+    rope_token_bwd_kernel(const __grid_constant__ RopeArgs a, int depth) {
+  extern __shared__ __align__(128) char dyn[];
+  int chunk, cta;
+  const int part = part_of(a, chunk, cta);
+  const RopePart& P = a.part[part];
+  const int lph = a.d / 16;
+  const TokenTeam team(P.heads * lph, 1);
+  if (team.id >= team.count) return;
+  const int tid = team.tid, threads = team.threads;
+  TokenSmem& sm = reinterpret_cast<TokenSmem*>(dyn)[team.id];
   const Lane l = lane_of<kHalves>(a, tid % lph);
   const bool on = tid < P.heads * lph;
   const int h0 = on ? tid / lph * a.d : 0;
-  const uint32_t stride = gridDim.x;
-  uint32_t n = blockIdx.x, fn = n;
-  const T* g = static_cast<const T*>(P.g) + (long long)n * P.ldg + h0;
-  const T* x = static_cast<const T*>(P.x) + (part < 2 ? (long long)n * P.ldx + h0 : 0);
-  T* o = static_cast<T*>(P.o) + (long long)n * P.ldo + h0;
-  const long long dg = (long long)stride * P.ldg, dout = (long long)stride * P.ldo,
-                  dx = part < 2 ? (long long)stride * P.ldx : 0;
-  char* weights = dyn;
-  char* ring = dyn + weight_bytes(1, threads);
+  const uint32_t stride = P.ctas * team.count;
+  const uint32_t row = cta * team.count + team.id;  // of partial sums
+  uint32_t n = row, fn = n;
   const int stage = Slot<T>::bytes(4, threads);
+  char* weights = dyn + team.count * (int)sizeof(TokenSmem) +
+                  team.id * (weight_bytes(1, threads) + depth * stage);
+  char* ring = weights + weight_bytes(1, threads);
   const uint32_t ring_at = shared_u32(ring);
   int to = 0, from = 0;
   auto fetch = [&]() {
     if (fn < a.tokens) {
+      const T* g = static_cast<const T*>(P.g) + (uint64_t)fn * (uint32_t)P.ldg + h0;
       Slot<T>::fetch(ring_at + to, g + l.ea, 0, threads, tid, on);
       Slot<T>::fetch(ring_at + to, g + l.eb, 1, threads, tid, on);
       if (part < 2) {
+        const T* x = static_cast<const T*>(P.x) + (uint64_t)fn * (uint32_t)P.ldx + h0;
         Slot<T>::fetch(ring_at + to, x + l.ea, 2, threads, tid, on);
         Slot<T>::fetch(ring_at + to, x + l.eb, 3, threads, tid, on);
       }
+      fn += stride;
     }
-    fn += stride;  // at most twice the CTAs past the tokens, far from 2^32
-    g += dg;
-    x += dx;
     copy_commit();
     to = depth == 2 ? stage - to : 0;
   };
@@ -776,99 +836,118 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_token_bwd_kernel(RopeArg
     Slot<T>::take(ring + from, j + 1, threads, tid, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
-  if (depth == 2) fetch();
   if (part == 2) {
-    for (; n < a.tokens; n += stride, o += dout) {
+    if (depth == 2) fetch();
+    for (; n < a.tokens; n += stride) {
       fetch();
       arrive();
       f2 A[4], B[4];
       take(0, A, B);
       from = depth == 2 ? stage - from : 0;
-      if (on) pack16<kHalves>(o, l, A, B);
+      if (on) pack16<kHalves>(static_cast<T*>(P.o) + (uint64_t)n * (uint32_t)P.ldo + h0, l, A, B);
     }
     return;
   }
-  Gather ang;
-  ang.init(a, n, stride, tid, threads);
-  ang.put(sm.cs[0], tid, threads);
+  TokenAngles ang;
+  ang.init(a, n, stride, tid, threads, sm);
+  ang.fetch(a, sm, 0, tid, threads);
+  ang.fetch(a, sm, 1, tid, threads);
+  copy_commit();
   f2 accA[4], accB[4];
   {
     f2 A[4], B[4];
     weight16<kHalves>(on ? P.w : nullptr, a.w_bf16, h0, l, A, B);
-    put_weights(weights, 0, threads, A, B);
+    put_weights(weights, 0, team, A, B);
 #pragma unroll
     for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
   }
-  part_sync(threads);
-  int buf = 0;
-  for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
+  copy_wait<0>();
+  team.sync();  // the first two tokens' angles
+  if (depth == 2) fetch();
+  int buf = 0, cs = 0;
+  for (; n < a.tokens; n += stride, buf ^= 1, cs = after(cs)) {
+    // the angles of the token after the next: every thread has waited for them
+    // when it comes to the next token's barrier
+    ang.fetch(a, sm, after(after(cs)), tid, threads);
     fetch();
     arrive();
     f2 XA[4], XB[4], GA[4], GB[4], s = pk(0.f, 0.f), d = s;
     {
       f2 C[4], S[4], A[4], B[4];
-      angles_of(sm.cs[buf], l, C, S);
+      angles_of(sm.cs[cs], l, C, S);
       take(0, A, B);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
         GB[i] = fma2(B[i], C[i], mul2(A[i], neg2(S[i])));
       }
+      one_by_one();
       take(2, XA, XB);
-      get_weights(weights, 0, threads, A, B);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s = fma2(XB[i], XB[i], fma2(XA[i], XA[i], s));
-        d = fma2(XB[i], mul2(GB[i], B[i]), fma2(XA[i], mul2(GA[i], A[i]), d));
-      }
+      for (int i = 0; i < 4; ++i) s = fma2(XB[i], XB[i], fma2(XA[i], XA[i], s));
+      one_by_one();
+      get_weights(weights, 0, 0, team, A);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d = fma2(XA[i], mul2(GA[i], A[i]), d);
+      one_by_one();
+      get_weights(weights, 0, 1, team, B);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d = fma2(XB[i], mul2(GB[i], B[i]), d);
     }
     from = depth == 2 ? stage - from : 0;
-    ang.ahead(a);  // the next token's angles, written ahead of the barrier
-    ang.put(sm.cs[buf ^ 1], tid, threads);
-    const float2 t = part_sum(make_float2(sum2(s), sum2(d)), sm, buf, threads);
+    const float2 t = part_sum(make_float2(sum2(s), sum2(d)), sm, buf, team);
+    const float inv = 1.f / (float)(P.heads * a.d);
     const float r = rsqrtf(t.x * inv + a.eps);
     const float c = -t.y * inv * r * r * r;
     const f2 rr = pk(r, r), cc = pk(c, c);
-    f2 WA[4], WB[4];
-    get_weights(weights, 0, threads, WA, WB);
+    f2 W[4];
+    get_weights(weights, 0, 0, team, W);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f2 pA = mul2(GA[i], rr), pB = mul2(GB[i], rr);
-      accA[i] = fma2(pA, XA[i], accA[i]);
-      accB[i] = fma2(pB, XB[i], accB[i]);
-      GA[i] = fma2(pA, WA[i], mul2(XA[i], cc));
-      GB[i] = fma2(pB, WB[i], mul2(XB[i], cc));
+      const f2 p = mul2(GA[i], rr);
+      accA[i] = fma2(p, XA[i], accA[i]);
+      GA[i] = fma2(p, W[i], mul2(XA[i], cc));
     }
-    if (on) pack16<kHalves>(o, l, GA, GB);
+    one_by_one();
+    get_weights(weights, 0, 1, team, W);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f2 p = mul2(GB[i], rr);
+      accB[i] = fma2(p, XB[i], accB[i]);
+      GB[i] = fma2(p, W[i], mul2(XB[i], cc));
+    }
+    if (on) pack16<kHalves>(static_cast<T*>(P.o) + (uint64_t)n * (uint32_t)P.ldo + h0, l, GA, GB);
   }
   dependents_may_start();
   if (P.part && on)
-    pack16<kHalves>(P.part + (long long)blockIdx.x * P.heads * a.d + h0, l, accA, accB);
+    pack16<kHalves>(P.part + (long long)row * P.heads * a.d + h0, l, accA, accB);
 }
 
 // out[c] = sum over rows of part[row][c], for two matrices in one launch
-// (blockIdx.y).  A CTA owns eight columns; 32 rows are read side by side and
+// (blockIdx.y).  A CTA owns eight columns; 128 rows are read side by side and
 // joined in a fixed order, so equal calls give equal bits.
 struct ColSum {
   const float* part;
   void* out;
   int rows, cols;
 };
-__global__ void __launch_bounds__(256) rope_colsum_kernel(ColSum s0, ColSum s1, int bf16) {
-  __shared__ float red[32][9];
+constexpr int kSumLanes = 128;
+__global__ void __launch_bounds__(8 * kSumLanes) rope_colsum_kernel(ColSum s0, ColSum s1,
+                                                                    int bf16) {
+  __shared__ float red[kSumLanes][9];
   wait_for_partial_sums();
   const ColSum s = blockIdx.y ? s1 : s0;
   const int c = blockIdx.x * 8 + (threadIdx.x & 7), lane = threadIdx.x >> 3;
   if (blockIdx.x * 8 >= s.cols || !s.out) return;  // cols is a multiple of 8
   float v = 0.f;
 #pragma unroll 8
-  for (int r = lane; r < s.rows; r += 32) v += s.part[(long long)r * s.cols + c];
+  for (int r = lane; r < s.rows; r += kSumLanes) v += s.part[(long long)r * s.cols + c];
   red[lane][threadIdx.x & 7] = v;
   __syncthreads();
   if (threadIdx.x < 8) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += red[i][threadIdx.x];
+    for (int i = 0; i < kSumLanes; ++i) v += red[i][threadIdx.x];
     store_param(s.out, bf16, c, v);
   }
 }
@@ -958,55 +1037,79 @@ basa_status check_rope(const basa_rope_params* p, bool bwd, RopeDims* r) {
   return BASA_OK;
 }
 
-// Launch shape: CTAs along the tokens, and the chunks and steps of each part.
+// Launch shape.  The CTAs of a part (q, k, v) number in proportion to its steps,
+// so that all end together and none carries its set-up for a handful of steps.
 struct RopeGrid {
-  unsigned x, y;
+  unsigned x;
   int threads, v;
-  int chunks[2], steps[2];
+  int ctas[3], chunks[3], steps[3];
+  int teams;    // norm over a token: most teams of a CTA
+  int rows[2];  // backward: rows of partial sums of q's and k's weights
 };
 
 RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bool bwd) {
   RopeGrid g;
+  memset(&g, 0, sizeof(g));
   const int sms = row_sm_count();
+  const int heads[3] = {r.heads[0], r.heads[1], r.heads[1]};
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
     const int units = p->H * p->d / 16;  // H >= Hkv
     g.v = bwd || units <= 64 ? 1 : 2;
     g.threads = ((units + g.v - 1) / g.v + 31) / 32 * 32;
-    g.chunks[0] = g.chunks[1] = 1;
-    g.steps[0] = g.steps[1] = 0;
-    g.y = with_v ? 3 : 2;
     // q's and k's CTAs on the SMs at a time (96 and 128 registers a thread); more
     // would only leave more rows of partial sums
-    const int per_sm = (bwd ? 320 : 640) / g.threads;
-    const long long cap = (long long)sms * (per_sm > 1 ? per_sm : 1);
-    g.x = (unsigned)(r.tokens < cap ? r.tokens : cap);
+    int per_sm = (bwd ? 320 : 640) / g.threads;
+    if (per_sm < 1) per_sm = 1;
+    for (int i = 0; i < (with_v ? 3 : 2); ++i) {
+      const int threads = ((heads[i] * p->d / 16 + g.v - 1) / g.v + 31) / 32 * 32;
+      int teams = g.threads / threads;
+      if (teams > kMaxTeams) teams = kMaxTeams;
+      if (teams > g.teams) g.teams = teams;
+      const long long need = (r.tokens + teams - 1) / teams;
+      long long ctas = (long long)sms * per_sm / teams;
+      if (ctas < sms) ctas = sms;
+      g.ctas[i] = (int)(need < ctas ? need : ctas);
+      g.chunks[i] = 1;
+      g.x += g.ctas[i];
+      if (i < 2) g.rows[i] = g.ctas[i] * teams;
+    }
     return g;
   }
   const int hpw = 512 / p->d;
   g.threads = kRopeThreads;
-  g.v = 0;
-  g.y = 0;
-  for (int i = 0; i < 2; ++i) {
-    const int steps = (r.heads[i] + hpw - 1) / hpw;
+  int all = 0;
+  for (int i = 0; i < (with_v ? 3 : 2); ++i) {
+    const int steps = (heads[i] + hpw - 1) / hpw;
     const int want = (steps + 7) / 8;
-    g.steps[i] = ((steps + want - 1) / want + 1) / 2 * 2;
+    g.steps[i] = (steps + want - 1) / want;
     g.chunks[i] = (steps + g.steps[i] - 1) / g.steps[i];
+    all += g.steps[i] * g.chunks[i];
   }
-  g.y = g.chunks[0] + g.chunks[1] + (with_v ? g.chunks[1] : 0);
   const long long need = (r.tokens + kRopeWarps - 1) / kRopeWarps;
-  const long long cap = (long long)sms * (bwd ? 8 : 32);
-  g.x = (unsigned)(need < cap ? need : cap);
+  // Forward, a warp takes as many tokens as make six steps, so long as the SMs have
+  // several CTAs each to choose from; backward, as few CTAs as balance, since
+  // each leaves a row of partial sums.
+  const long long budget = (long long)sms * (bwd ? 12 : 20);
+  for (int i = 0; i < (with_v ? 3 : 2); ++i) {
+    const long long ctas = (budget * g.steps[i] + all - 1) / all;
+    long long each = need / ctas > 1 ? need / ctas : 1;  // tokens of a warp, for all alike
+    const long long most = (5 + g.steps[i]) / g.steps[i];
+    if (!bwd && each > most) each = most;
+    g.ctas[i] = (int)((need + each - 1) / each);
+    g.x += g.ctas[i] * g.chunks[i];
+    if (i < 2) g.rows[i] = g.ctas[i] * g.chunks[i];
+  }
   return g;
 }
 
 size_t rope_part_bytes(const basa_rope_params* p, const RopeDims& r, const RopeGrid& g, int i) {
   const size_t cols = p->norm == BASA_ROPE_NORM_TOKEN ? (size_t)r.heads[i] * p->d : (size_t)p->d;
-  return up256((size_t)g.x * g.chunks[i] * cols * sizeof(float));
+  return up256((size_t)g.rows[i] * cols * sizeof(float));
 }
 
 template <typename TI, typename TO, int kLph>
 void go_head(const RopeGrid& g, const RopeArgs& a, bool halves, bool norm, cudaStream_t st) {
-  const dim3 grid(g.x, g.y);
+  const dim3 grid(g.x);
   if (halves && norm) rope_head_kernel<TI, TO, kLph, true, true><<<grid, kRopeThreads, 0, st>>>(a);
   else if (halves) rope_head_kernel<TI, TO, kLph, true, false><<<grid, kRopeThreads, 0, st>>>(a);
   else if (norm) rope_head_kernel<TI, TO, kLph, false, true><<<grid, kRopeThreads, 0, st>>>(a);
@@ -1014,7 +1117,7 @@ void go_head(const RopeGrid& g, const RopeArgs& a, bool halves, bool norm, cudaS
 }
 template <typename T, int kLph>
 void go_head_bwd(const RopeGrid& g, const RopeArgs& a, bool halves, bool norm, cudaStream_t st) {
-  const dim3 grid(g.x, g.y);
+  const dim3 grid(g.x);
   if (halves && norm) rope_head_bwd_kernel<T, kLph, true, true><<<grid, kRopeThreads, 0, st>>>(a);
   else if (halves) rope_head_bwd_kernel<T, kLph, true, false><<<grid, kRopeThreads, 0, st>>>(a);
   else if (norm) rope_head_bwd_kernel<T, kLph, false, true><<<grid, kRopeThreads, 0, st>>>(a);
@@ -1030,15 +1133,15 @@ bool allow(K kernel, int smem) {
 template <typename K, typename... Args>
 bool go_token(K kernel, const RopeGrid& g, int smem, cudaStream_t st, const Args&... args) {
   if (!allow(kernel, smem)) return false;
-  kernel<<<dim3(g.x, g.y), g.threads, smem, st>>>(args...);
+  kernel<<<g.x, g.threads, smem, st>>>(args...);
   return true;
 }
 template <typename TI, typename TO>
 bool go_fwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
   const bool halves = p->layout == BASA_ROPE_HALVES;
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
-    const int smem =
-        weight_bytes(g.v, g.threads) + kStages<TI> * Slot<TI>::bytes(2 * g.v, g.threads);
+    const int smem = g.teams * (int)sizeof(TokenSmem) + weight_bytes(g.v, g.threads) +
+                     kStages<TI> * Slot<TI>::bytes(2 * g.v, g.threads);
     if (g.v == 1)
       return halves ? go_token(rope_token_kernel<TI, TO, 1, true>, g, smem, st, a)
                     : go_token(rope_token_kernel<TI, TO, 1, false>, g, smem, st, a);
@@ -1055,8 +1158,9 @@ template <typename T>
 bool go_bwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cudaStream_t st) {
   const bool halves = p->layout == BASA_ROPE_HALVES;
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
-    const int w = weight_bytes(1, g.threads), stage = Slot<T>::bytes(4, g.threads);
-    const int depth = w + 2 * stage <= 220 * 1024 ? 2 : 1;  // fp32 rows of over 11 K values: 1
+    const int w = g.teams * (int)sizeof(TokenSmem) + weight_bytes(1, g.threads);
+    const int stage = Slot<T>::bytes(4, g.threads);
+    const int depth = w + 2 * stage <= 224 * 1024 ? 2 : 1;  // fp32 rows of over 11 K values: 1
     const int smem = w + depth * stage;
     if (g.threads <= 320)
       return halves ? go_token(rope_token_bwd_kernel<T, 320, 2, true>, g, smem, st, a, depth)
@@ -1085,19 +1189,19 @@ RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid&
   a.d = p->d;
   a.eps = p->eps;
   a.w_bf16 = p->w_dtype == BASA_BF16;
-  RopePart* part[3] = {&a.q, &a.k, &a.v};
   const int64_t in[3] = {p->ldq, p->ldk, p->ldv}, gr[3] = {p->ldgq, p->ldgk, p->ldgv};
   const float ds[3] = {p->q_descale, p->k_descale, p->v_descale};
   for (int i = 0; i < 3; ++i) {
     const int j = i > 0;
     const long long row = (long long)r.heads[j] * p->d;
-    part[i]->heads = r.heads[j];
-    part[i]->chunks = g.chunks[j];
-    part[i]->steps = g.steps[j];
-    part[i]->ldx = in[i] ? in[i] : row;
-    part[i]->ldg = row;
-    part[i]->ldo = bwd && gr[i] ? gr[i] : row;
-    part[i]->mul = 1.f / (ds[i] > 0.f ? ds[i] : 1.f);
+    a.part[i].heads = r.heads[j];
+    a.part[i].ctas = g.ctas[i];
+    a.part[i].chunks = g.chunks[i];
+    a.part[i].steps = g.steps[i];
+    a.part[i].ldx = in[i] ? in[i] : row;
+    a.part[i].ldg = row;
+    a.part[i].ldo = bwd && gr[i] ? gr[i] : row;
+    a.part[i].mul = 1.f / (ds[i] > 0.f ? ds[i] : 1.f);
   }
   return a;
 }
@@ -1158,9 +1262,9 @@ basa_status basa_qkv_rope(const void* q, const void* k, const void* v, const voi
     return BASA_ERR_ALIGN;
   const RopeGrid g = rope_grid(p, r, v != nullptr, false);
   RopeArgs a = rope_args(p, r, g, table, false);
-  a.q.x = q; a.k.x = k; a.v.x = v;
-  a.q.w = q_weight; a.k.w = k_weight;
-  a.q.o = q_out; a.k.o = k_out; a.v.o = v_out;
+  a.part[0].x = q; a.part[1].x = k; a.part[2].x = v;
+  a.part[0].w = q_weight; a.part[1].w = k_weight;
+  a.part[0].o = q_out; a.part[1].o = k_out; a.part[2].o = v_out;
   const bool low = p->out_dtype == BASA_FP8_E4M3;
   const bool ok = p->dtype == BASA_BF16
                       ? (low ? go_fwd<__nv_bfloat16, e4m3_t>(p, g, a, stream)
@@ -1176,8 +1280,13 @@ size_t basa_qkv_rope_bwd_workspace_size(const basa_rope_params* p) {
   if (check_rope(p, true, &r) != BASA_OK || p->norm == BASA_ROPE_NORM_NONE ||
       r.tokens * p->H == 0)
     return 0;
-  const RopeGrid g = rope_grid(p, r, true, true);
-  return rope_part_bytes(p, r, g, 0) + rope_part_bytes(p, r, g, 1);
+  size_t n = 0;
+  for (int v = 0; v < 2; ++v) {  // with and without v
+    const RopeGrid g = rope_grid(p, r, v != 0, true);
+    const size_t m = rope_part_bytes(p, r, g, 0) + rope_part_bytes(p, r, g, 1);
+    n = m > n ? m : n;
+  }
+  return n;
 }
 
 basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,
@@ -1213,24 +1322,22 @@ basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void
   const bool sums = dq_weight || dk_weight;
   if (sums && !workspace) return BASA_ERR_WORKSPACE;
   if (sums && off16(workspace)) return BASA_ERR_ALIGN;
-  // the grid, and with it the order of the weights' sums, does not go by v
-  RopeGrid g = rope_grid(p, r, true, true);
-  if (!dv) g.y -= token ? 1 : g.chunks[1];
+  const RopeGrid g = rope_grid(p, r, dv != nullptr, true);
   RopeArgs a = rope_args(p, r, g, table, true);
-  a.q.x = q; a.k.x = k;
-  a.q.g = dq_out; a.k.g = dk_out; a.v.g = dv_out;
-  a.q.w = q_weight; a.k.w = k_weight;
-  a.q.o = dq; a.k.o = dk; a.v.o = dv;
+  a.part[0].x = q; a.part[1].x = k;
+  a.part[0].g = dq_out; a.part[1].g = dk_out; a.part[2].g = dv_out;
+  a.part[0].w = q_weight; a.part[1].w = k_weight;
+  a.part[0].o = dq; a.part[1].o = dk; a.part[2].o = dv;
   char* ws = static_cast<char*>(workspace);
-  if (dq_weight) a.q.part = reinterpret_cast<float*>(ws);
-  if (dk_weight) a.k.part = reinterpret_cast<float*>(ws + rope_part_bytes(p, r, g, 0));
+  if (dq_weight) a.part[0].part = reinterpret_cast<float*>(ws);
+  if (dk_weight) a.part[1].part = reinterpret_cast<float*>(ws + rope_part_bytes(p, r, g, 0));
   const bool ok = p->dtype == BASA_BF16 ? go_bwd<__nv_bfloat16>(p, g, a, stream)
                                         : go_bwd<float>(p, g, a, stream);
   if ((s = launched()) != BASA_OK || !ok) return BASA_ERR_CUDA;
   if (sums) {
-    const ColSum c0{a.q.part, dq_weight, (int)g.x * g.chunks[0], cols[0]};
-    const ColSum c1{a.k.part, dk_weight, (int)g.x * g.chunks[1], cols[1]};
-    return launch_dependent(rope_colsum_kernel, dim3((unsigned)(cols[0] / 8), 2), 256, stream, c0,
+    const ColSum c0{a.part[0].part, dq_weight, g.rows[0], cols[0]};
+    const ColSum c1{a.part[1].part, dk_weight, g.rows[1], cols[1]};
+    return launch_dependent(rope_colsum_kernel, dim3((unsigned)(cols[0] / 8), 2), 8 * kSumLanes, stream, c0,
                             c1, (int)(p->w_dtype == BASA_BF16));
   }
   return BASA_OK;

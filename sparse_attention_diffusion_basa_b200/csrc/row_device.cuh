@@ -241,6 +241,17 @@ __device__ __forceinline__ float2 lane_sum(float2 v) {
   return v;
 }
 
+// The same value, but one that the compiler takes for a new one: what is formed
+// from it inside a loop is not moved ahead of the loop, where it would hold
+// registers that the loop does not have.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+// Keeps the compiler from loading all of a sequence's operands ahead of using
+// the first, for the same reason.
+__device__ __forceinline__ void one_by_one() { asm volatile("" ::: "memory"); }
+
 // Programmatic dependent launch: a kernel that ends a gradient's sums is launched
 // while the one that leaves the partial sums still runs, and waits for it.
 __device__ __forceinline__ void dependents_may_start() {
