@@ -1054,11 +1054,11 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
   const int heads[3] = {r.heads[0], r.heads[1], r.heads[1]};
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
     const int units = p->H * p->d / 16;  // H >= Hkv
-    g.v = bwd || units <= 64 ? 1 : 2;
+    g.v = bwd || units <= 128 ? 1 : 2;
     g.threads = ((units + g.v - 1) / g.v + 31) / 32 * 32;
     // q's and k's CTAs on the SMs at a time (96 and 128 registers a thread); more
     // would only leave more rows of partial sums
-    int per_sm = (bwd ? 320 : 640) / g.threads;
+    int per_sm = (bwd ? 320 : g.v == 1 ? 960 : 640) / g.threads;
     if (per_sm < 1) per_sm = 1;
     for (int i = 0; i < (with_v ? 3 : 2); ++i) {
       const int threads = ((heads[i] * p->d / 16 + g.v - 1) / g.v + 31) / 32 * 32;
