@@ -578,14 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int r0 = (int)(a.rows * blockIdx.x / gridDim.x);
   const int r1 = (int)(a.rows * (blockIdx.x + 1) / gridDim.x);
   const long long off = (long long)r0 * a.C;
-  const TX* px = kNorm ? static_cast<const TX*>(a.x) + off : nullptr;
-  const TY* pgh = kNorm ? static_cast<const TY*>(a.gh) + off : nullptr;
+  long long src = off;  // of the next row to fetch
   // gx and y may be absent: zeros, and the address of an output that is not read
-  const TX* pgx = static_cast<const TX*>(a.gx ? a.gx : a.dx) + off;
-  const TY* py = kBranch ? static_cast<const TY*>(a.need_y ? a.y : a.dy) + off : nullptr;
   const bool have_gx = a.gx != nullptr, have_y = a.need_y;
-  TX* dx = static_cast<TX*>(a.dx) + off;
-  TY* dy = kBranch ? static_cast<TY*>(a.dy) + off : nullptr;
+  long long dst = off;  // of the rows at work
   long long g = r0 / a.group;
   int ahead = r0, ahead_end = (int)min((long long)r1, (g + 1) * a.group), at_stage = 0;
   auto fetch = [&](int to) {
@@ -595,22 +591,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kR; ++k) {
         const uint32_t at = ring_at + to + k * row_bytes;
         const bool on = k == 0 || ahead + k < ahead_end;
-        const long long e = on ? (long long)k * a.C : 0;
+        const long long e = src + (on ? k * a.C : 0);
         if (kNorm) {
-          lx.fetch(at + o_x, px + e, c, on);
-          ly.fetch(at + o_gh, pgh + e, c, on);
+          lx.fetch(at + o_x, static_cast<const TX*>(a.x) + e, c, on);
+          ly.fetch(at + o_gh, static_cast<const TY*>(a.gh) + e, c, on);
         }
-        lx.fetch(at, pgx + e, c, on && have_gx);
-        if (kBranch) ly.fetch(at + o_y, py + e, c, on && have_y);
+        lx.fetch(at, static_cast<const TX*>(have_gx ? a.gx : a.dx) + e, c, on && have_gx);
+        if (kBranch)
+          ly.fetch(at + o_y, static_cast<const TY*>(have_y ? a.y : a.dy) + e, c, on && have_y);
       }
       const int rows = min(kR, ahead_end - ahead);
-      const int step = rows * a.C;
-      if (kNorm) {
-        px += step;
-        pgh += step;
-      }
-      pgx += step;
-      if (kBranch) py += step;
+      src += rows * a.C;
       ahead += rows;
       if (ahead == ahead_end) ahead_end = (int)min((long long)r1, ahead + a.group);
     }
@@ -733,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[k][j][i] = mul2(res, gx[i]);
-        if (c.ok(j) && on[k]) put_row(dx + k * a.C + c.col(j), v[k][j], a.wide);
+        if (c.ok(j) && on[k]) put_row(static_cast<TX*>(a.dx) + dst + k * a.C + c.col(j), v[k][j], a.wide);
         if (kBranch) {
           f2 yh[4];
           ly.take(row + o_y, j, c, yh);
@@ -743,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum.d[j][i] = fma2(gx[i], yh[i], sum.d[j][i]);
               v[k][j][i] = mul2(gx[i], G[i]);
             }
-            if (c.ok(j) && on[k]) put_row(dy + k * a.C + c.col(j), v[k][j], a.wide);
+            if (c.ok(j) && on[k]) put_row(static_cast<TY*>(a.dy) + dst + k * a.C + c.col(j), v[k][j], a.wide);
           } else {
             const f2 pm = both(-st[k].z), ps = both(st[k].w);
 #pragma unroll
@@ -776,14 +767,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[k][j][i] = mul2(ps, fma2(mul2(add2(yh[i], pm), ps), c2, add2(v[k][j][i], c1)));
-          if (c.ok(j) && on[k]) put_row(dy + k * a.C + c.col(j), v[k][j], a.wide);
+          if (c.ok(j) && on[k]) put_row(static_cast<TY*>(a.dy) + dst + k * a.C + c.col(j), v[k][j], a.wide);
         }
       }
     }
     fetch(at_stage);
     at_stage = at_stage + stage == a.depth * stage ? 0 : at_stage + stage;
-    dx += rows * a.C;
-    if (kBranch) dy += rows * a.C;
+    dst += rows * a.C;
     r += rows;
   }
 }

@@ -1089,7 +1089,7 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
   // Forward, a warp takes as many tokens as make six steps, so long as the SMs have
   // several CTAs each to choose from; backward, as few CTAs as balance, since
   // each leaves a row of partial sums.
-  const long long budget = (long long)sms * (bwd ? 12 : 20);
+  const long long budget = (long long)sms * (bwd ? 12 : 10);
   for (int i = 0; i < (with_v ? 3 : 2); ++i) {
     const long long ctas = (budget * g.steps[i] + all - 1) / all;
     long long each = need / ctas > 1 ? need / ctas : 1;  // tokens of a warp, for all alike
