@@ -908,9 +908,7 @@ constexpr int kSmem = 224 * 1024;  // of an SM's 228 KB, beside static parts and
 
 template <typename K>
 basa_status go(K kernel, const GnArgs& a, unsigned grid, int threads, int smem, cudaStream_t st) {
-  if (smem > 32 * 1024 &&  // beside the static part, 48 KB are free to take
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return BASA_ERR_CUDA;
+  if (!allow_smem(kernel, smem)) return BASA_ERR_CUDA;
   kernel<<<grid, threads, smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
 }

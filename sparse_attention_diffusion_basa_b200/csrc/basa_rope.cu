@@ -292,7 +292,8 @@ template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
 // across tokens.  The norm's weight is folded into the angles:
 // A' = r (A (wA cos) - B (wB sin)).
 template <typename TI, typename TO, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 5)
+    rope_head_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<TI>;
   constexpr int kStage = Slot<TI>::bytes(2, 32);
   __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
@@ -395,7 +396,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_head_kernel(const __grid
 // in a lane's own sixteen columns over all its tokens and heads, then over the
 // CTA, and left as one row of partial sums a CTA.
 template <typename T, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_head_bwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4)
+    rope_head_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<T>;
   constexpr int kStage = Slot<T>::bytes(kNorm ? 4 : 2, 32);
   __shared__ __align__(16) char rings[kRopeWarps][kDepth * kStage];
@@ -554,7 +556,7 @@ struct TokenSmem {
 // rotated are (1, 0) in every buffer from the start.
 struct TokenAngles {
   Coord at;
-  int spot[2];  // base of the pair in the table, axis in the two highest bits
+  uint32_t spot[2];  // base of the pair in the table, axis in the two highest bits
   __device__ __forceinline__ void init(const RopeArgs& a, uint32_t n, uint32_t step, int tid,
                                        int threads, TokenSmem& sm) {
     at.init(a, n, step);
@@ -562,7 +564,7 @@ struct TokenAngles {
     for (int i = 0; i < 2; ++i) {
       const int j = tid + i * threads;
       const Spot s = spot_of(a, j < 64 ? j : -1);
-      spot[i] = s.base | s.axis << 30;
+      spot[i] = (uint32_t)s.base | (uint32_t)s.axis << 30;
       if (s.axis == 3 && j < 64) {
 #pragma unroll
         for (int b = 0; b < kCs; ++b)
@@ -575,13 +577,13 @@ struct TokenAngles {
                                         int threads) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t axis = (uint32_t)spot[i] >> 30;
+      const uint32_t axis = spot[i] >> 30;
       if (axis != 3u) {
         const int off = axis == 0u ? (int)at.t * a.nt : axis == 1u ? (int)at.y * a.nh
                                                                    : (int)at.x * a.nw;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
                          shared_u32(sm.cs[buf]) + (tid + i * threads) * 8),
-                     "l"(a.table + (spot[i] & 0x3fffffff) + off)
+                     "l"(a.table + (int)(spot[i] & 0x3fffffffu) + off)
                      : "memory");
       }
     }
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
 // out[c] = sum over rows of part[row][c], for two matrices in one launch
 // (blockIdx.y).  A CTA owns eight columns; 128 rows are read side by side and
-// joined in a fixed order, so equal calls give equal bits.
+// joined pairwise, in a fixed order, so equal calls give equal bits.
 struct ColSum {
   const float* part;
   void* out;
@@ -934,20 +936,31 @@ struct ColSum {
 constexpr int kSumLanes = 128;
 __global__ void __launch_bounds__(8 * kSumLanes) rope_colsum_kernel(ColSum s0, ColSum s1,
                                                                     int bf16) {
-  __shared__ float red[kSumLanes][9];
+  __shared__ float red[kSumLanes / 4][8], red2[kSumLanes / 16][8];
   wait_for_partial_sums();
   const ColSum s = blockIdx.y ? s1 : s0;
-  const int c = blockIdx.x * 8 + (threadIdx.x & 7), lane = threadIdx.x >> 3;
+  const int k = threadIdx.x & 7, lane = threadIdx.x >> 3, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 8 + k;
   if (blockIdx.x * 8 >= s.cols || !s.out) return;  // cols is a multiple of 8
   float v = 0.f;
 #pragma unroll 8
   for (int r = lane; r < s.rows; r += kSumLanes) v += s.part[(long long)r * s.cols + c];
-  red[lane][threadIdx.x & 7] = v;
+  auto over_warp = [](float x) {  // the warp's four rows
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+  };
+  v = over_warp(v);
+  if ((threadIdx.x & 31) < 8) red[warp][k] = v;
+  __syncthreads();
+  if (threadIdx.x < 2 * kSumLanes) {  // whole warps
+    v = over_warp(red[lane][k]);
+    if ((threadIdx.x & 31) < 8) red2[warp][k] = v;
+  }
   __syncthreads();
   if (threadIdx.x < 8) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSumLanes; ++i) v += red[i][threadIdx.x];
+    for (int i = 0; i < kSumLanes / 16; ++i) v += red2[i][k];
     store_param(s.out, bf16, c, v);
   }
 }
@@ -1123,16 +1136,9 @@ void go_head_bwd(const RopeGrid& g, const RopeArgs& a, bool halves, bool norm, c
   else if (norm) rope_head_bwd_kernel<T, kLph, false, true><<<grid, kRopeThreads, 0, st>>>(a);
   else rope_head_bwd_kernel<T, kLph, false, false><<<grid, kRopeThreads, 0, st>>>(a);
 }
-// Dynamic shared memory beyond what a kernel may use unasked has to be allowed.
-template <typename K>
-bool allow(K kernel, int smem) {
-  return smem <= 32 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
-             cudaSuccess;
-}
 template <typename K, typename... Args>
 bool go_token(K kernel, const RopeGrid& g, int smem, cudaStream_t st, const Args&... args) {
-  if (!allow(kernel, smem)) return false;
+  if (!allow_smem(kernel, smem)) return false;
   kernel<<<g.x, g.threads, smem, st>>>(args...);
   return true;
 }

@@ -276,7 +276,21 @@ basa_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaS
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? BASA_OK : BASA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess) return BASA_OK;
+  cudaGetLastError();  // reported here, not by the next call
+  return BASA_ERR_CUDA;
+}
+
+// Dynamic shared memory beyond what a kernel may use unasked (48 KB with its
+// static part) has to be allowed.
+template <typename K>
+bool allow_smem(K kernel, int smem) {
+  if (smem <= 32 * 1024 ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+          cudaSuccess)
+    return true;
+  cudaGetLastError();
+  return false;
 }
 
 inline int row_sm_count() {

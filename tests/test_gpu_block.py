@@ -6,9 +6,9 @@ K * 2^-24 times the sum of the magnitudes it was formed from, K counting the
 roundings on the longest chain: a row's sum adds at most 32 values in a thread,
 5 times over a warp's lanes and 20 times over a CTA's warps, and about ten
 further roundings stand around it, so K = 64 + 2.  A column sum of a gradient adds
-along a thread's rows (at most 12 in these cases), the CTA's 8 warps, and
-partial rows of every CTA (at most 1184 in 32 chains of 37, joined by 32):
-K = 128.  Each rounding to the output's type adds half a step of the value, and
+along a thread's rows (at most 28 in these cases), the CTA's 8 warps, and
+partial rows of every CTA (at most 1776 in 32 chains or more, each of at most 56,
+joined by 32 or fewer): K = 128.  Each rounding to the output's type adds half a step of the value, and
 for e4m3 no less than half its smallest step, 2^-10."""
 import math
 
@@ -135,6 +135,10 @@ ROPE = [
     (2, (2, 3, 5), 7, 7, 128, (32, 48, 48), None, "halves", F32, F32, None, False, 13),
     (1, (1, 9, 10), 3, 3, 64, (0, 32, 32), None, "halves", BF, BF, None, True, 14),
     (1, (1, 45, 31), 33, 11, 64, (0, 24, 40), "head", "pairs", BF, BF, BF, True, 15),
+    # a token's heads shared between CTAs
+    (1, (1, 6, 7), 40, 10, 128, (16, 56, 56), "head", "pairs", BF, BF, BF, True, 20),
+    (1, (2, 3, 2), 200, 100, 32, (4, 12, 16), "head", "halves", BF, BF, F32, False, 21),
+    (1, (1, 2, 5), 72, 72, 64, (0, 32, 32), None, "pairs", F32, F32, None, False, 22),
     # e4m3 outputs
     (1, (1, 8, 9), 8, 2, 128, (16, 56, 56), "head", "pairs", BF, E4, BF, True, 16),
     (2, (2, 3, 5), 4, 4, 128, (32, 48, 48), "token", "halves", BF, E4, F32, False, 17),
@@ -219,6 +223,30 @@ def test_rope_backward(basa, case):
     for a, b in zip((again[0], again[1], again[3], again[4]), (dq, dk, dqw, dkw)):
         assert (a is None and b is None) or torch.equal(a, b)
     assert again[2] is None
+
+
+@pytest.mark.parametrize("norm,H,Hkv", [("head", 24, 8), ("token", 12, 3), ("token", 40, 40), (None, 5, 5)])
+def test_rope_many_tokens(basa, norm, H, Hkv):
+    """More tokens than warps and teams at a time: each takes several, across rows and frames."""
+    B, grid, d, axes = 2, (5, 31, 67), 128, (44, 42, 42)
+    q, k = rnd(1, B, *grid, H, d, dtype=BF), rnd(2, B, *grid, Hkv, d, dtype=BF)
+    gq, gk = rnd(3, B, *grid, H, d, dtype=BF), rnd(4, B, *grid, Hkv, d, dtype=BF)
+    n = {"head": (d, d), "token": (H * d, Hkv * d)}.get(norm)
+    qw, kw = (rnd(5 + i, m, mean=1.0, std=0.3) for i, m in enumerate(n)) if norm else (None, None)
+    table = basa.rope_table(grid, axes)
+    cs = table64(table, grid, axes)
+    args = dict(norm=norm, q_weight=qw, k_weight=kw)
+    qo, ko, _ = basa.qkv_rope(q, k, None, table, axes, **args)
+    dq, dk, _, dqw, dkw = basa.qkv_rope_bwd(gq, gk, None, q, k, table, axes, **args)
+    for x, g, w, o, dx, dw, name in ((q, gq, qw, qo, dq, dqw, "q"), (k, gk, kw, ko, dk, dkw, "k")):
+        ref, mag = rope64(x, w, cs, axes, "pairs", norm, 1e-6)
+        check(o, ref, mag, K_ROW, name)
+        ref, mag, wref, wmag = rope_bwd64(g, x, w, cs, axes, "pairs", norm, 1e-6)
+        check(dx, ref, mag, K_ROW, f"d{name}")
+        if w is not None:
+            # a thread adds at most 20770 tokens' heads / (148 CTAs * 4 warps * 4 heads a step) < 180 terms,
+            # and at most 2368 partial rows in 128 chains of 19, joined by 12
+            check(dw, wref, wmag, 180 + 8 + 19 + 12 + K_ROW, f"d{name}_weight")
 
 
 def test_rope_gradients_against_differences(basa):
@@ -573,6 +601,12 @@ def test_border_backward_gives_the_same_bits(basa, case):
 @pytest.mark.parametrize("C", [256, 5120])
 def test_border_groups(basa, lead, nmod, C):
     case = (lead, C, (BF, BF), nmod, F32, F32, "gate scale shift weight bias post_weight", "layer", "rms", 1.0, 77)
+    x, y, p = border_inputs(case)
+    n = x.numel() // C
+    xo, h = basa.gated_norm(x, y, norm="layer", post_norm="rms", eps=1e-5, **p)
+    rx, rh, _, mag, hmag = border64(x.double().view(n, C), y.double().view(n, C), p, "layer", "rms", 1e-5, 1e-6, 1.0)
+    check(xo.view(n, C), rx, mag, K_ROW, "x_out")
+    check(h.view(n, C), rh, hmag, K_ROW, "h")
     got, ref, p = border_grads(basa, case)
     for name in ("dgate", "dscale", "dshift", "dweight", "dbias", "dpost_weight"):
         want, mag = ref[name]
@@ -623,6 +657,52 @@ def test_border_in_place_and_expanded(basa):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     with pytest.raises(ValueError, match="leading dims"):
         basa.gated_norm(x, y, gate=gate, scale=scale)
+
+
+def test_border_outputs_at_16_bytes(basa):
+    """fp32 outputs aligned to 16 bytes but not to 32, rows that end inside a warp, guards around them."""
+    n, C = 37, 712
+    x, y = rnd(1, n, C), rnd(2, n, C)
+    want = basa.gated_norm(x, y, post_norm="layer")
+    buf = torch.full((2, n * C + 16), 9.0, device="cuda")
+    outs = [b[4:4 + n * C].view(n, C) for b in buf]
+    got = basa.gated_norm(x, y, post_norm="layer", x_out=outs[0], h_out=outs[1])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert (buf[:, :4] == 9.0).all() and (buf[:, 4 + n * C:] == 9.0).all()
+
+
+def test_border_backward_writes_nothing_else(basa):
+    """The C entry on guarded buffers, with one workspace for two calls of different shapes."""
+    from sparse_attention_diffusion_basa_b200 import _lib
+    import ctypes
+    lib = _lib.load()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for rows, groups, C in ((333, 3, 1000), (35, 7, 264)):
+        f = lambda seed, *s: rnd(seed, *s, dtype=BF)  # noqa: E731
+        x, y, gh, gx = (f(i, rows, C) for i in range(4))
+        mods, w = [f(10 + i, groups, C) for i in range(3)], [f(20 + i, C) for i in range(3)]
+        st = torch.cat([torch.zeros(rows, 1, device="cuda"), torch.ones(rows, 1, device="cuda")] * 2, 1).contiguous()
+        sizes = [rows * C, rows * C, groups * C, C, C, C, groups * C, groups * C]
+        bufs = [torch.full((s + 64,), 3.0, dtype=BF, device="cuda") for s in sizes]
+        outs = [b[32:32 + s] for b, s in zip(bufs, sizes)]
+        prm = _lib.BasaGnormParams(rows, groups, C, 1, 2, 1e-6, 1e-6, 1.0, 1, 1, 1, 1, C, C, C)
+        assert lib.basa_gated_norm_bwd_workspace_size(ctypes.byref(prm)) <= ws.numel()
+        p = lambda t: t.data_ptr()  # noqa: E731
+        code = lib.basa_gated_norm_bwd(p(gh), p(x), p(st), p(y), p(gx), p(mods[0]), p(w[0]), p(w[1]), p(w[2]),
+                                       p(mods[1]), *(p(o) for o in outs), p(ws), ctypes.byref(prm),
+                                       torch.cuda.current_stream().cuda_stream)
+        assert code == 0
+        torch.cuda.synchronize()
+        view = lambda t: t.view(groups, rows // groups, C)  # noqa: E731
+        g = basa.gated_norm_bwd(view(gh), view(x), st.view(groups, -1, 4), view(y), view(gx), gate=mods[0],
+                                post_weight=w[0], weight=w[1], bias=w[2], scale=mods[1], shift=mods[2],
+                                norm="layer", post_norm="rms")
+        for a, b in zip(g, outs):
+            assert torch.equal(a.reshape(-1), b)
+        for b, s in zip(bufs, sizes):
+            assert (b[:32] == 3.0).all() and (b[32 + s:] == 3.0).all()
+            assert torch.isfinite(b).all() and not (b[32:32 + s] == 3.0).all()
 
 
 def test_border_far_mean(basa):
