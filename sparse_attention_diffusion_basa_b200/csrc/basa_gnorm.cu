@@ -433,15 +433,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           s = both(post.y);
         }
         const f2 res = both(a.res);
+        const bool plain = a.post == BASA_NORM_NONE && a.res == 1.f;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           f2 u[4], G[4];
           py.take(at + x_bytes, j, c, u);
           px.take(at, j, c, f[j]);
           get8(sG + c.at(j), half, G);
+          if (plain) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            f[j][i] = fma2(mul2(add2(u[i], m), s), G[i], mul2(res, f[j][i]));
+            for (int i = 0; i < 4; ++i) f[j][i] = fma2(u[i], G[i], f[j][i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              f[j][i] = fma2(mul2(add2(u[i], m), s), G[i], mul2(res, f[j][i]));
+          }
           if (c.ok(j)) put_row(xo + c.col(j), f[j], a.wide);
           one_by_one();
         }
