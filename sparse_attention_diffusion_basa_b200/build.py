@@ -29,7 +29,7 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "-shared", "-cudart", "static",
-    "--threads", "0", "--split-compile", "0",  # files, and the kernels of a file, side by side
+    "--threads", "0",  # files side by side (--split-compile leaves registers to the number of cores)
 ]
 
 

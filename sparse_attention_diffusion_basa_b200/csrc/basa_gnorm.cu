@@ -13,10 +13,14 @@
 //   dscale = w A + b S, dshift = S, dgate = pw D
 //   dw = sum (1 + scale) A, db = sum (1 + scale) S, dpw = sum gate D.
 //
-// HBM-bound: every row is read and written once.  A CTA takes whole rows, each
-// thread the same columns of every row, so the modulations of a run of rows and
-// the column sums of the backward stay in registers; a CTA's rows are a
-// contiguous range, read ahead by asynchronous copies.
+// Bound by HBM: every row is read and written once.  A CTA takes whole rows, each
+// thread the same columns of every row; a CTA's rows are a contiguous range, so a
+// modulation row's factors are formed once for many rows, and rows are read ahead
+// by asynchronous copies.  Measured on a B200 (copy 6.57 TB/s), device time of the
+// call: 75600 rows of 5120, fp32 stream and bf16 branch 791 us = 5.87 TB/s (89% of
+// the copy rate; the first form, unpacked and one row at a time, 1172); 14508 rows
+// of 1536 bf16, both norms, a modulation a frame 42 us (65%; about 8 us of it start
+// and end); backward of 16384 rows of 5120 bf16 190 us = 5.30 TB/s (81%; 273).
 #include <math.h>
 #include <string.h>
 
@@ -329,6 +333,9 @@ __device__ __forceinline__ float2 row_stats(const f2 (&f)[kV][4], const Cols& c,
 // of exchanges that several rows at a time hide.  The factors of a modulation
 // row are combined once, in fp32, into shared memory for all the teams (direct:
 // a modulation covers too few rows for that, and each team keeps its own).
+// One row at a time a CTA took 939 us for 75600 rows of 5120, teams 791; rows dealt
+// to the CTAs in turn instead of in ranges the same there, and 61 us instead of 42
+// for 14508 rows of 1536, where each CTA then meets every frame's factors.
 // ---------------------------------------------------------------------------
 constexpr int kFwdThreads = 512;  // 128 registers each
 
@@ -785,7 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial sums of gnorm_bwd_kernel.  A CTA owns eight columns and
-// reads 32 partial rows side by side, joined in a fixed order.  blockIdx.z = 0:
+// reads 32 partial rows side by side, joined in a fixed order, so equal calls give
+// equal bits.  It reads a few MB that still lie in the L2 (8 us cold for 16384 rows of
+// 5120) and is launched while the rows' kernel ends.  blockIdx.z = 0:
 // the modulation rows whose tokens span several CTAs; blockIdx.y is the
 // modulation row, or, where there are more of those than CTAs, the CTA in which
 // the row begins (each CTA's range splits at most one that goes on behind it).

@@ -9,6 +9,17 @@
 //   forward   (a cos - b sin, a sin + b cos)
 //   backward  gn = the output's gradient turned by minus the angle,
 //             dx = r (w gn - x r^2 mean(w gn x)),  dw = sum over rows of gn x r.
+//
+// Bound by HBM: every row is read once and written once.  At 6.5 TB/s an SM moves
+// 23 bytes a clock, so the kernels also have to spend few instructions a value:
+// arithmetic is packed two values an instruction, a lane holds both elements of
+// its pairs, a token's angles are gathered once for all its heads, and rows come
+// by asynchronous copies that need no registers while they are under way.
+// Measured on a B200 (copy 6.57 TB/s), device time of the call: 128 x 128 grid, 24
+// heads of 128 in bf16, q, k, v slices of one projection 96.1 us = 6.28 TB/s (96% of
+// the copy rate); 21 x 45 x 80 clip, norm over 40 heads, q and k 503 us = 6.16 TB/s
+// (94%; the first form, unpacked and with an exchange between lanes a pair, 684);
+// backward of two 128 x 128 grids 260 us = 6.20 TB/s (94%; first form 389).
 #include <math.h>
 #include <string.h>
 
@@ -290,7 +301,8 @@ template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
 // token, so that a token's angles are read once for all its heads.  Rows come
 // through a ring of asynchronous copies, private to each lane, that runs ahead
 // across tokens.  The norm's weight is folded into the angles:
-// A' = r (A (wA cos) - B (wB sin)).
+// A' = r (A (wA cos) - B (wB sin)).  Five CTAs an SM at 96 registers against
+// four at 128: 96 and 101 us for the 128 x 128 grid.
 template <typename TI, typename TO, int kLph, bool kHalves, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, 5)
     rope_head_kernel(const __grid_constant__ RopeArgs a) {
@@ -394,7 +406,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
 
 // Backward of rope_head_kernel, the same walk.  The weight's gradient is summed
 // in a lane's own sixteen columns over all its tokens and heads, then over the
-// CTA, and left as one row of partial sums a CTA.
+// CTA, and left as one row of partial sums a CTA.  Four CTAs an SM: 128 registers
+// hold the sums and a step without spills; two 128 x 128 grids with 24 heads 260 us.
 template <typename T, int kLph, bool kHalves, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, 4)
     rope_head_bwd_kernel(const __grid_constant__ RopeArgs a) {
@@ -539,7 +552,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 // token's angles are gathered by one thread a pair into shared memory and read
 // behind the barrier that the row's sum needs anyway.  The weights' columns of a
 // thread lie in shared memory too (fp32, read by that thread alone): in
-// registers they would halve the CTAs of an SM.
+// registers they would halve the CTAs of an SM.  Two groups of sixteen a thread
+// beyond 2048 columns, fewer barriers and angles a value: 503 us for the 21 x 45 x 80
+// clip with 40 heads of 128, one group 640; up to 2048 one, for more rows at a time:
+// a clip of 14508 tokens with 12 query and 4 K/V heads 43 us, two groups 49.  Four
+// times the SMs in CTAs of each part (three are resident): 503 us, three times 517,
+// six times 511.
 constexpr int kCs = 5;  // kStages + 1 of bf16
 struct TokenSmem {
   float2 red[2][32];
@@ -575,6 +593,7 @@ struct TokenAngles {
   // Of the coordinates' token, which then move on to the next.
   __device__ __forceinline__ void fetch(const RopeArgs& a, TokenSmem& sm, int buf, int tid,
                                         int threads) {
+    if (tid >= 64) return;  // at most 64 pairs: none of them this warp's
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t axis = spot[i] >> 30;
@@ -786,7 +805,12 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 
 // Backward of rope_token_kernel.  Both sums of a row (x^2 and w gn x) share one
 // barrier; a thread's columns of the weight's gradient stay in registers over
-// all its tokens and are left as one row of partial sums a CTA.
+// all its tokens and are left as one row of partial sums a team.  Up to 5120
+// columns two CTAs of 320 threads share an SM without a spilled register (57 us
+// for a clip of 14508 tokens with 12 query and 4 K/V heads of 128, first form 99); up
+// to 8192 one CTA; beyond, 64 registers a thread and spills.  What bounds it there is
+// latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, at 20
+// warps an SM.
 template <typename T, int kThreads, int kCtas, bool kHalves>
 __global__ void __launch_bounds__(kThreads, kCtas)
     rope_token_bwd_kernel(const __grid_constant__ RopeArgs a, int depth) {
@@ -1100,8 +1124,9 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
   }
   const long long need = (r.tokens + kRopeWarps - 1) / kRopeWarps;
   // Forward, a warp takes as many tokens as make six steps, so long as the SMs have
-  // several CTAs each to choose from; backward, as few CTAs as balance, since
-  // each leaves a row of partial sums.
+  // several CTAs each to choose from (budgets of 5, 20 and 40 CTAs an SM were slower
+  // than 10); backward, as few CTAs as balance, since each leaves a row of partial
+  // sums.
   const long long budget = (long long)sms * (bwd ? 12 : 10);
   for (int i = 0; i < (with_v ? 3 : 2); ++i) {
     const long long ctas = (budget * g.steps[i] + all - 1) / all;
