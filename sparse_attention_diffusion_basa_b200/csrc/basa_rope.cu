@@ -40,6 +40,7 @@ struct RopePart {      // one of q, k, v
   int chunks;          // CTAs that share a token's heads
   int steps;           // of 512 / d heads each, per chunk
   float mul;           // e4m3 output: 1 / descale
+  float inv;           // 1 / values of a token's row
 };
 
 struct RopeArgs {
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 // registers they would halve the CTAs of an SM.  Two groups of sixteen a thread
 // beyond 2048 columns, fewer barriers and angles a value: 503 us for the 21 x 45 x 80
 // clip with 40 heads of 128, one group 640; up to 2048 one, for more rows at a time:
-// a clip of 14508 tokens with 12 query and 4 K/V heads 43 us, two groups 49.  Four
+// a clip of 14508 tokens with 12 query and 4 K/V heads 41 us, two groups 49.  Four
 // times the SMs in CTAs of each part (three are resident): 503 us, three times 517,
 // six times 511.
 constexpr int kCs = 5;  // kStages + 1 of bf16
@@ -627,6 +628,16 @@ struct TokenTeam {
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
   }
 };
+// Sums over a team, each warp's left in red and read by all behind the barrier.  One
+// sum: teams of up to eight warps read all eight (zeros beyond the team's), wider
+// ones exchange once more.  Two sums: always by exchanges, which need fewer
+// registers (a spilled one costs the backward 18%).
+__device__ __forceinline__ void clear_sums(TokenSmem& sm, const TokenTeam& t) {
+  if (t.tid < 16) {
+    const int b = t.tid >> 3, i = t.tid & 7;
+    if (i >= t.threads >> 5) reinterpret_cast<float*>(sm.red[b])[i] = 0.f;
+  }
+}
 __device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, const TokenTeam& t) {
   // the lanes of each half keep one of the two sums and hand on the other
   const int lane = threadIdx.x & 31;
@@ -648,9 +659,15 @@ __device__ __forceinline__ float2 part_sum(float2 v, TokenSmem& sm, int buf, con
 __device__ __forceinline__ float part_sum(float v, TokenSmem& sm, int buf, const TokenTeam& t) {
   v = lane_sum<32>(v);
   const int lane = threadIdx.x & 31;
-  if (lane == 0) sm.red[buf][t.tid >> 5].x = v;
+  float* red = reinterpret_cast<float*>(sm.red[buf]);
+  if (lane == 0) red[t.tid >> 5] = v;
   t.sync();
-  return lane_sum<32>(lane < t.threads >> 5 ? sm.red[buf][lane].x : 0.f);
+  if (t.threads <= 256) {
+    const float4* w = reinterpret_cast<const float4*>(red);
+    const float4 a = w[0], b = w[1];
+    return sum2(add2(add2(pk(a.x, a.y), pk(a.z, a.w)), add2(pk(b.x, b.y), pk(b.z, b.w))));
+  }
+  return lane_sum<16>((lane & 15) < t.threads >> 5 ? red[lane & 15] : 0.f);
 }
 
 // A thread's weights in shared memory: eight 16-byte pieces for each of its kV
@@ -689,7 +706,6 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   if (team.id >= team.count) return;
   const int tid = team.tid, threads = team.threads;
   TokenSmem& sm = reinterpret_cast<TokenSmem*>(dyn)[team.id];
-  const float inv = 1.f / (float)(P.heads * a.d);
   const Lane l = lane_of<kHalves>(a, tid % lph);
   const int h0 = tid / lph * a.d, dh = threads / lph * a.d;  // a thread's heads, in elements
   const uint32_t stride = P.ctas * team.count;
@@ -752,6 +768,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   }
   TokenAngles ang;
   ang.init(a, n, stride, tid, threads, sm);
+  clear_sums(sm, team);
 #pragma unroll
   for (int s = 0; s < kDepth - 1; ++s) {
     ang.fetch(a, sm, s, tid, threads);
@@ -776,7 +793,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
       for (int i = 0; i < 4; ++i) s = fma2(B[j][i], B[j][i], fma2(A[j][i], A[j][i], s));
     }
     from = from + stage == kDepth * stage ? 0 : from + stage;
-    const float r = mul * rsqrtf(part_sum(sum2(s), sm, buf, team) * inv + a.eps);
+    const float r = mul * rsqrtf(part_sum(sum2(s), sm, buf, team) * P.inv + a.eps);
     const f2 rr = pk(r, r);
     f2 C[4], S[4], N[4];  // N = -S
     angles_of(sm.cs[cs], l, C, S);
@@ -809,8 +826,8 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 // columns two CTAs of 320 threads share an SM without a spilled register (57 us
 // for a clip of 14508 tokens with 12 query and 4 K/V heads of 128, first form 99); up
 // to 8192 one CTA; beyond, 64 registers a thread and spills.  What bounds it there is
-// latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, at 20
-// warps an SM.
+// latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, at twelve
+// to fifteen warps an SM.
 template <typename T, int kThreads, int kCtas, bool kHalves>
 __global__ void __launch_bounds__(kThreads, kCtas)
     rope_token_bwd_kernel(const __grid_constant__ RopeArgs a, int depth) {
@@ -876,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   TokenAngles ang;
   ang.init(a, n, stride, tid, threads, sm);
-  ang.fetch(a, sm, 0, tid, threads);
+    ang.fetch(a, sm, 0, tid, threads);
   ang.fetch(a, sm, 1, tid, threads);
   copy_commit();
   f2 accA[4], accB[4];
@@ -1093,9 +1110,10 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
     const int units = p->H * p->d / 16;  // H >= Hkv
     g.v = bwd || units <= 128 ? 1 : 2;
     g.threads = ((units + g.v - 1) / g.v + 31) / 32 * 32;
-    // q's and k's CTAs on the SMs at a time (96 and 128 registers a thread); more
-    // would only leave more rows of partial sums
-    int per_sm = (bwd ? 320 : g.v == 1 ? 960 : 640) / g.threads;
+    // q's and k's CTAs on the SMs at a time; backward, more would only leave more
+    // rows of partial sums; forward, threads of a part on an SM: 640 against 960 and
+    // 1280 41.0, 43.6 and 47.1 us (14508 tokens, 12 query and 4 K/V heads of 128)
+    int per_sm = (bwd ? 320 : 640) / g.threads;
     if (per_sm < 1) per_sm = 1;
     for (int i = 0; i < (with_v ? 3 : 2); ++i) {
       const int threads = ((heads[i] * p->d / 16 + g.v - 1) / g.v + 31) / 32 * 32;
@@ -1232,6 +1250,7 @@ RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid&
     a.part[i].ldx = in[i] ? in[i] : row;
     a.part[i].ldg = row;
     a.part[i].ldo = bwd && gr[i] ? gr[i] : row;
+    a.part[i].inv = 1.f / (float)row;
     a.part[i].mul = 1.f / (ds[i] > 0.f ? ds[i] : 1.f);
   }
   return a;
