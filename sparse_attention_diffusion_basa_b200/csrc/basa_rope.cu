@@ -556,7 +556,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 // registers they would halve the CTAs of an SM.  Two groups of sixteen a thread
 // beyond 2048 columns, fewer barriers and angles a value: 503 us for the 21 x 45 x 80
 // clip with 40 heads of 128, one group 640; up to 2048 one, for more rows at a time:
-// a clip of 14508 tokens with 12 query and 4 K/V heads 41 us, two groups 49.  Four
+// a clip of 14508 tokens with 12 query and 4 K/V heads 43 us, two groups 49 (33 since
+// several teams share a CTA).  Four
 // times the SMs in CTAs of each part (three are resident): 503 us, three times 517,
 // six times 511.
 constexpr int kCs = 5;  // kStages + 1 of bf16
@@ -670,25 +671,26 @@ __device__ __forceinline__ float part_sum(float v, TokenSmem& sm, int buf, const
   return lane_sum<16>((lane & 15) < t.threads >> 5 ? red[lane & 15] : 0.f);
 }
 
-// A thread's weights in shared memory: eight 16-byte pieces for each of its kV
-// groups of sixteen (A's, then B's), the team's threads side by side.
-__device__ __forceinline__ void put_weights(char* at, int j, const TokenTeam& t, const f2 (&A)[4],
+// A warp keeps its weights and its stages side by side in shared memory, 512 bytes a
+// piece, sixteen a lane: every offset is a constant of the instruction.
+// Weights: eight 16-byte pieces for each of a lane's kV groups of sixteen (A's,
+// then B's).
+__device__ __forceinline__ void put_weights(char* at, int j, int lane, const f2 (&A)[4],
                                             const f2 (&B)[4]) {
-  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + j * 4 * t.threads + t.tid;
+  ulonglong2* w = reinterpret_cast<ulonglong2*>(at) + j * 4 * 32 + lane;
   w[0] = make_ulonglong2(A[0], A[1]);
-  w[t.threads] = make_ulonglong2(A[2], A[3]);
-  w[2 * t.threads] = make_ulonglong2(B[0], B[1]);
-  w[3 * t.threads] = make_ulonglong2(B[2], B[3]);
+  w[32] = make_ulonglong2(A[2], A[3]);
+  w[64] = make_ulonglong2(B[0], B[1]);
+  w[96] = make_ulonglong2(B[2], B[3]);
 }
 // Group j's A (second = 0) or B (1).
-__device__ __forceinline__ void get_weights(const char* at, int j, int second, const TokenTeam& t,
+__device__ __forceinline__ void get_weights(const char* at, int j, int second, int lane,
                                             f2 (&W)[4]) {
-  const ulonglong2* w =
-      reinterpret_cast<const ulonglong2*>(at) + (j * 4 + 2 * second) * t.threads + t.tid;
+  const ulonglong2* w = reinterpret_cast<const ulonglong2*>(at) + (j * 4 + 2 * second) * 32 + lane;
   ulonglong2 v = w[0];
   W[0] = v.x;
   W[1] = v.y;
-  v = w[t.threads];
+  v = w[32];
   W[2] = v.x;
   W[3] = v.y;
 }
@@ -714,10 +716,11 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   bool on[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) on[j] = j * threads + tid < units;
-  const int stage = Slot<TI>::bytes(2 * kV, threads);
+  constexpr int stage = Slot<TI>::bytes(2 * kV, 32);
+  const int lane = tid & 31;
   char* weights = dyn + team.count * (int)sizeof(TokenSmem) +
-                  team.id * (weight_bytes(kV, threads) + kDepth * stage);
-  char* ring = weights + weight_bytes(kV, threads);
+                  (team.id * threads + tid) / 32 * (weight_bytes(kV, 32) + kDepth * stage);
+  char* ring = weights + weight_bytes(kV, 32);
   const uint32_t ring_at = shared_u32(ring);
   int to = 0, from = 0;
   auto fetch = [&]() {
@@ -726,8 +729,8 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
         const TI* head = x + (on[j] ? h0 + j * dh : 0);
-        Slot<TI>::fetch(ring_at + to, head + l.ea, 2 * j, threads, tid, on[j]);
-        Slot<TI>::fetch(ring_at + to, head + l.eb, 2 * j + 1, threads, tid, on[j]);
+        Slot<TI>::fetch(ring_at + to, head + l.ea, 2 * j, 32, lane, on[j]);
+        Slot<TI>::fetch(ring_at + to, head + l.eb, 2 * j + 1, 32, lane, on[j]);
       }
       fn += stride;
     }
@@ -736,8 +739,8 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   };
   auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
     Raw8<TI> ra, rb;
-    Slot<TI>::take(ring + from, 2 * j, threads, tid, ra);
-    Slot<TI>::take(ring + from, 2 * j + 1, threads, tid, rb);
+    Slot<TI>::take(ring + from, 2 * j, 32, lane, ra);
+    Slot<TI>::take(ring + from, 2 * j + 1, 32, lane, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
   const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
@@ -778,7 +781,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   for (int j = 0; j < kV; ++j) {
     f2 A[4], B[4];
     weight16<kHalves>(on[j] ? P.w : nullptr, a.w_bf16, h0 + j * dh, l, A, B);
-    put_weights(weights, j, team, A, B);
+    put_weights(weights, j, lane, A, B);
   }
   int buf = 0, cs = 0, cs_to = kDepth - 1;
   for (; n < a.tokens; n += stride, buf ^= 1, cs = after(cs), cs_to = after(cs_to)) {
@@ -807,8 +810,8 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       f2 WA[4], WB[4];
-      get_weights(weights, j, 0, team, WA);
-      get_weights(weights, j, 1, team, WB);
+      get_weights(weights, j, 0, lane, WA);
+      get_weights(weights, j, 1, lane, WB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 p = mul2(A[j][i], WA[i]), q = mul2(B[j][i], WB[i]);
@@ -823,11 +826,11 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 // Backward of rope_token_kernel.  Both sums of a row (x^2 and w gn x) share one
 // barrier; a thread's columns of the weight's gradient stay in registers over
 // all its tokens and are left as one row of partial sums a team.  Up to 5120
-// columns two CTAs of 320 threads share an SM without a spilled register (57 us
+// columns two CTAs of 320 threads share an SM without a spilled register (51 us
 // for a clip of 14508 tokens with 12 query and 4 K/V heads of 128, first form 99); up
 // to 8192 one CTA; beyond, 64 registers a thread and spills.  What bounds it there is
-// latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, at twelve
-// to fifteen warps an SM.
+// latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, and each
+// CTA's set-up.
 template <typename T, int kThreads, int kCtas, bool kHalves>
 __global__ void __launch_bounds__(kThreads, kCtas)
     rope_token_bwd_kernel(const __grid_constant__ RopeArgs a, int depth) {
@@ -846,21 +849,22 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const uint32_t stride = P.ctas * team.count;
   const uint32_t row = cta * team.count + team.id;  // of partial sums
   uint32_t n = row, fn = n;
-  const int stage = Slot<T>::bytes(4, threads);
+  constexpr int stage = Slot<T>::bytes(4, 32);
+  const int lane = tid & 31;
   char* weights = dyn + team.count * (int)sizeof(TokenSmem) +
-                  team.id * (weight_bytes(1, threads) + depth * stage);
-  char* ring = weights + weight_bytes(1, threads);
+                  (team.id * threads + tid) / 32 * (weight_bytes(1, 32) + depth * stage);
+  char* ring = weights + weight_bytes(1, 32);
   const uint32_t ring_at = shared_u32(ring);
   int to = 0, from = 0;
   auto fetch = [&]() {
     if (fn < a.tokens) {
       const T* g = static_cast<const T*>(P.g) + (uint64_t)fn * (uint32_t)P.ldg + h0;
-      Slot<T>::fetch(ring_at + to, g + l.ea, 0, threads, tid, on);
-      Slot<T>::fetch(ring_at + to, g + l.eb, 1, threads, tid, on);
+      Slot<T>::fetch(ring_at + to, g + l.ea, 0, 32, lane, on);
+      Slot<T>::fetch(ring_at + to, g + l.eb, 1, 32, lane, on);
       if (part < 2) {
         const T* x = static_cast<const T*>(P.x) + (uint64_t)fn * (uint32_t)P.ldx + h0;
-        Slot<T>::fetch(ring_at + to, x + l.ea, 2, threads, tid, on);
-        Slot<T>::fetch(ring_at + to, x + l.eb, 3, threads, tid, on);
+        Slot<T>::fetch(ring_at + to, x + l.ea, 2, 32, lane, on);
+        Slot<T>::fetch(ring_at + to, x + l.eb, 3, 32, lane, on);
       }
       fn += stride;
     }
@@ -875,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   };
   auto take = [&](int j, f2(&A)[4], f2(&B)[4]) {
     Raw8<T> ra, rb;
-    Slot<T>::take(ring + from, j, threads, tid, ra);
-    Slot<T>::take(ring + from, j + 1, threads, tid, rb);
+    Slot<T>::take(ring + from, j, 32, lane, ra);
+    Slot<T>::take(ring + from, j + 1, 32, lane, rb);
     unpack16<kHalves>(ra, rb, A, B);
   };
   if (part == 2) {
@@ -900,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   {
     f2 A[4], B[4];
     weight16<kHalves>(on ? P.w : nullptr, a.w_bf16, h0, l, A, B);
-    put_weights(weights, 0, team, A, B);
+    put_weights(weights, 0, lane, A, B);
 #pragma unroll
     for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
   }
@@ -929,11 +933,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(XB[i], XB[i], fma2(XA[i], XA[i], s));
       one_by_one();
-      get_weights(weights, 0, 0, team, A);
+      get_weights(weights, 0, 0, lane, A);
 #pragma unroll
       for (int i = 0; i < 4; ++i) d = fma2(XA[i], mul2(GA[i], A[i]), d);
       one_by_one();
-      get_weights(weights, 0, 1, team, B);
+      get_weights(weights, 0, 1, lane, B);
 #pragma unroll
       for (int i = 0; i < 4; ++i) d = fma2(XB[i], mul2(GB[i], B[i]), d);
     }
@@ -944,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const float c = -t.y * inv * r * r * r;
     const f2 rr = pk(r, r), cc = pk(c, c);
     f2 W[4];
-    get_weights(weights, 0, 0, team, W);
+    get_weights(weights, 0, 0, lane, W);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f2 p = mul2(GA[i], rr);
@@ -952,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       GA[i] = fma2(p, W[i], mul2(XA[i], cc));
     }
     one_by_one();
-    get_weights(weights, 0, 1, team, W);
+    get_weights(weights, 0, 1, lane, W);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f2 p = mul2(GB[i], rr);
@@ -1110,10 +1114,19 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
     const int units = p->H * p->d / 16;  // H >= Hkv
     g.v = bwd || units <= 128 ? 1 : 2;
     g.threads = ((units + g.v - 1) / g.v + 31) / 32 * 32;
-    // q's and k's CTAs on the SMs at a time; backward, more would only leave more
-    // rows of partial sums; forward, threads of a part on an SM: 640 against 960 and
-    // 1280 41.0, 43.6 and 47.1 us (14508 tokens, 12 query and 4 K/V heads of 128)
-    int per_sm = (bwd ? 320 : 640) / g.threads;
+    // Several teams to a CTA where one is a few warps: CTAs of a warp or two come and
+    // go one by one, and a few CTAs of many warps spread over an SM more evenly.  4800
+    // tokens of 8 heads of 64, one team to a CTA and several: 34.8 and 12.3 us, backward
+    // 34.9 and 20.5; 14508 tokens with 12 query and 4 K/V heads of 128: 41.0 and 32.8,
+    // backward 57.4 and 51.0.
+    const int most = bwd ? 192 : 256;
+    int q_teams = g.threads < most ? most / g.threads : 1;
+    if (q_teams > kMaxTeams) q_teams = kMaxTeams;
+    g.threads *= q_teams;
+    // Threads of a part on an SM at a time.  Forward, at the 14508 tokens above (one
+    // team to a CTA), 640 against 960 and 1280: 41.0, 43.6 and 47.1 us; backward, where
+    // more leave more rows of partial sums, 384 against 192 and 576: 51.0, 70.5, 56.1.
+    int per_sm = (bwd ? 384 : 640) / g.threads;
     if (per_sm < 1) per_sm = 1;
     for (int i = 0; i < (with_v ? 3 : 2); ++i) {
       const int threads = ((heads[i] * p->d / 16 + g.v - 1) / g.v + 31) / 32 * 32;
@@ -1121,7 +1134,7 @@ RopeGrid rope_grid(const basa_rope_params* p, const RopeDims& r, bool with_v, bo
       if (teams > kMaxTeams) teams = kMaxTeams;
       if (teams > g.teams) g.teams = teams;
       const long long need = (r.tokens + teams - 1) / teams;
-      long long ctas = (long long)sms * per_sm / teams;
+      long long ctas = (long long)sms * per_sm * q_teams / teams;
       if (ctas < sms) ctas = sms;
       g.ctas[i] = (int)(need < ctas ? need : ctas);
       g.chunks[i] = 1;
