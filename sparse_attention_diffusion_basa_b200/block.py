@@ -25,8 +25,9 @@ _E4M3 = torch.float8_e4m3fn
 
 # The small calls of a sampler are bound by this file, not by their kernels, so
 # the checks of a call's shapes, strides, types and devices and the parameter
-# struct they lead to are kept (lru_cache) by just these: never by a tensor, its
-# address or its values.
+# struct they lead to are kept (lru_cache) by just these and by the numbers given,
+# as Python numbers: never by a tensor, its address or its values.  A factor held in
+# a 0-dim tensor hashes by identity, so numbers are converted ahead of the lookup.
 _KEPT = 512
 
 
@@ -49,6 +50,14 @@ def _code(table, key, name):
         return table[key]
     except (KeyError, TypeError):
         raise ValueError(f"{name} must be one of {sorted(map(str, table))}, got {key!r}") from None
+
+
+def _ints(xs):
+    return tuple(map(int, xs))
+
+
+def _floats(xs):
+    return tuple(map(float, xs))
 
 
 def _raw_stream(index: int) -> int:
@@ -171,10 +180,10 @@ def _rope_params(q, k, axes, layout, norm, eps, out_dtype, descale, lds, w_dtype
     if H != Hkv and (Hkv == 0 or H % Hkv):
         raise ValueError(f"q heads {H} must be a multiple of k/v heads {Hkv}")
     T, Hg, Wg = q[1:4] if len(q) == 6 else (1, 1, q[1])
-    at, ah, aw = (int(a) for a in axes)
+    at, ah, aw = axes
     return BasaRopeParams(q[0], H, Hkv, T, Hg, Wg, q[-1], at, ah, aw, _code(BASA_ROPE_LAYOUT, layout, "layout"),
-                          _code(BASA_ROPE_NORM, norm, "norm"), float(eps), _DT[dtype], _DT[out_dtype],
-                          _DT[w_dtype], *(float(x) for x in descale), *lds)
+                          _code(BASA_ROPE_NORM, norm, "norm"), eps, _DT[dtype], _DT[out_dtype],
+                          _DT[w_dtype], *descale, *lds)
 
 
 def _pairs(prm) -> int:
@@ -213,8 +222,7 @@ def _weights(q, k, q_weight, k_weight, norm):
 
 @functools.lru_cache(maxsize=_KEPT)
 def _table_plan(grid, axes, out):
-    T, Hg, Wg = (int(g) for g in grid)
-    at, ah, aw = (int(a) for a in axes)
+    (T, Hg, Wg), (at, ah, aw) = grid, axes
     d = 32
     while d < at + ah + aw and d < 128:
         d *= 2
@@ -234,7 +242,7 @@ def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(
     if stream is not None:
         with torch.cuda.stream(stream):
             return rope_table(grid, axes, theta, start, step, device, out)
-    plan = _table_plan(tuple(grid), tuple(axes), _meta(out))
+    plan = _table_plan(_ints(grid), _ints(axes), _meta(out))
     if out is None:
         dev = torch.device("cuda" if device is None else device)
         if dev.type != "cuda":
@@ -289,7 +297,7 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
                             eps=eps, out_dtype=out_dtype, descale=descale, out=out)
     outs = None if out is None else tuple(_meta(o) for o in out)
     plan = _rope_plan(_meta(q), _meta(k), _meta(v), _meta(q_weight), _meta(k_weight), _meta(table), outs,
-                      tuple(axes), layout, norm, eps, out_dtype, tuple(descale))
+                      _ints(axes), layout, norm, float(eps), out_dtype, _floats(descale))
     dev = q.device
     if out is None:
         dt = plan.dtype
@@ -344,7 +352,7 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
                                 q_weight=q_weight, k_weight=k_weight, eps=eps, out=out, workspace=workspace)
     outs = None if out is None else tuple(_meta(o) for o in out)
     plan = _rope_bwd_plan(_meta(dq_out), _meta(dk_out), _meta(dv_out), _meta(q), _meta(k), _meta(q_weight),
-                          _meta(k_weight), _meta(table), outs, tuple(axes), layout, norm, eps)
+                          _meta(k_weight), _meta(table), outs, _ints(axes), layout, norm, float(eps))
     dev = dq_out.device
     if out is None:
         dq, dk, dv = _like(dq_out), _like(dk_out), None if dv_out is None else _like(dv_out)
@@ -425,7 +433,7 @@ def _gnorm_params(x, y_dtype, mods, weights, norm, post_norm, eps, post_eps, res
             raise TypeError("weight, bias and post_weight must share a dtype")
         w_dtype = w[2]
     return BasaGnormParams(_numel(x[0][:-1]), max(groups or 1, 1), C, _code(BASA_NORM, norm, "norm"),
-                           _code(BASA_NORM, post_norm, "post_norm"), float(eps), float(post_eps), float(res_scale),
+                           _code(BASA_NORM, post_norm, "post_norm"), eps, post_eps, res_scale,
                            _DT[x[2]], _DT[y_dtype], _DT[mod_dtype or torch.float32],
                            _DT[w_dtype or torch.float32], *lds)
 
@@ -482,7 +490,7 @@ def gated_norm(x, y=None, *, gate=None, post_weight=None, weight=None, bias=None
                               h_out=h_out)
     plan = _gnorm_plan(_meta(x), _meta(y), (_meta(gate), _meta(scale), _meta(shift)),
                        (_meta(post_weight), _meta(weight), _meta(bias)), _meta(x_out), _meta(h_out), norm, post_norm,
-                       eps, post_eps, res_scale, h_dtype)
+                       float(eps), float(post_eps), float(res_scale), h_dtype)
     dev = x.device
     if x_out is None and y is not None:
         x_out = _like(x)
@@ -542,7 +550,7 @@ def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_wei
                                   res_scale=res_scale, workspace=workspace)
     plan = _gnorm_bwd_plan(_meta(dh), _meta(x_out), _meta(stats), _meta(y), _meta(dx_out),
                            (_meta(gate), _meta(scale), _meta(shift)),
-                           (_meta(post_weight), _meta(weight), _meta(bias)), norm, post_norm, res_scale)
+                           (_meta(post_weight), _meta(weight), _meta(bias)), norm, post_norm, float(res_scale))
     ref = x_out if x_out is not None else dx_out
     dev = ref.device
     dx = _like(ref)

@@ -1,0 +1,100 @@
+"""What the binding of the calls around the attention (qkv_rope, gated_norm and their backwards)
+makes of its arguments, on the host: tensors are stood in for by their shapes and made-up addresses,
+and the library's entry by a function that records the parameter struct, so nothing is launched."""
+import ctypes
+import gc
+import weakref
+
+import pytest
+import torch
+
+from sparse_attention_diffusion_basa_b200 import block
+
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+SIZE = {BF: 2, F32: 4, E4: 1}
+
+
+class Stub:
+    """A CUDA tensor as far as the binding looks at one."""
+    _next = 1 << 32
+
+    def __init__(self, *shape, dtype=BF, stride=None, at=None, device="cuda:0"):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self._stride = tuple(torch.empty(shape, device="meta").stride()) if stride is None else stride
+        if at is None:
+            at = Stub._next
+            Stub._next += 1 << 32
+        self._at = at
+
+    def stride(self):
+        return self._stride
+
+    def data_ptr(self):
+        return self._at
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The parameter structs of the calls that reach the library, copied as they were then."""
+    from sparse_attention_diffusion_basa_b200 import build
+    build.build()
+    seen = []
+
+    def on(device, fn, what, *args):
+        p = args[-1]._obj
+        seen.append(type(p).from_buffer_copy(bytes(p)))
+    monkeypatch.setattr(block, "_on", on)
+    monkeypatch.setattr(block, "_like", lambda t, dtype=None: Stub(*t.shape, dtype=dtype or t.dtype))
+    return seen
+
+
+def same32(got, value):
+    return got == ctypes.c_float(value).value
+
+
+def test_scalar_tensors_are_read_at_every_call(calls):
+    """A 0-dim tensor that is changed in place between two calls: the second call takes its new value."""
+    q, k, v = Stub(1, 1, 4, 4, 2, 64), Stub(1, 1, 4, 4, 2, 64), Stub(1, 1, 4, 4, 2, 64)
+    x, y = Stub(1, 6, 64), Stub(1, 6, 64)
+    st = Stub(1, 6, 4, dtype=F32)
+    cases = [
+        (("q_descale",), lambda s: block.qkv_rope(q, k, v, out_dtype=E4, descale=(s, 1.0, 1.0))),
+        (("k_descale", "v_descale"), lambda s: block.qkv_rope(q, k, v, out_dtype=E4, descale=[1.0, s, s])),
+        (("eps",), lambda s: block.qkv_rope(q, k, v, norm="head", eps=s)),
+        (("eps",), lambda s: block.qkv_rope_bwd(q, k, v, q, k, norm="head", eps=s)),
+        (("eps",), lambda s: block.gated_norm(x, y, eps=s)),
+        (("post_eps",), lambda s: block.gated_norm(x, y, post_norm="rms", post_eps=s)),
+        (("res_scale",), lambda s: block.gated_norm(x, y, res_scale=s)),
+        (("res_scale",), lambda s: block.gated_norm_bwd(x, x, st, y, res_scale=s)),
+    ]
+    for fields, call in cases:
+        s = torch.tensor(0.25)
+        for value in (0.25, 0.5, 0.125):
+            s.fill_(value)
+            call(s)
+            assert all(same32(getattr(calls[-1], f), value) for f in fields), (fields, value)
+
+
+def test_whole_number_tensors_are_read_at_every_call(calls):
+    n, m = torch.tensor(16), torch.tensor(48)
+    q, table = Stub(1, 1, 4, 4, 2, 64), Stub(4 * 32, 2, dtype=F32)
+    for rows, columns in ((16, 48), (48, 16), (32, 32)):
+        n.fill_(rows)
+        m.fill_(columns)
+        block.qkv_rope(q, q, None, table, (0, n, m))
+        assert (calls[-1].ah, calls[-1].aw) == (rows, columns)
+        block.qkv_rope_bwd(q, q, None, None, None, table, (0, n, m))
+        assert (calls[-1].ah, calls[-1].aw) == (rows, columns)
+        block.rope_table((1, n, m), (0, 8, 8), out=Stub(4 * 64, 2, dtype=F32))
+        assert (calls[-1].Hg, calls[-1].Wg) == (rows, columns)
+
+
+def test_no_scalar_tensor_is_kept(calls):
+    q, x = Stub(1, 1, 4, 4, 2, 64), Stub(1, 6, 64)
+    s = torch.tensor(0.5)
+    kept = weakref.ref(s)
+    block.qkv_rope(q, q, q, out_dtype=E4, norm="head", descale=(s, s, s), eps=s)
+    block.gated_norm(x, x, eps=s, post_eps=s, res_scale=s)
+    del s
+    gc.collect()
+    assert kept() is None
