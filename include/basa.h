@@ -343,8 +343,9 @@ typedef struct basa_rope_params {
   int32_t out_dtype;   /* of q_out, k_out, v_out: dtype, or BASA_FP8_E4M3 (forward only) */
   int32_t w_dtype;     /* of the norm weights and their gradients: BASA_F32 or BASA_BF16 */
   float q_descale, k_descale, v_descale; /* e4m3 outputs: an element's value is its e4m3 value
-                          times this factor (0 selects 1), as basa_window_attn takes it; values
-                          beyond the type's largest are stored as the largest */
+                          times this factor (0 selects 1; else from 2^-100 to 2^100), as
+                          basa_window_attn takes it.  Stored is value / factor; beyond the
+                          type's largest, the largest */
   int64_t ldq, ldk, ldv;    /* elements from one token's row of q, k, v to the next: a multiple
                           of 8 that holds the row; 0 selects dense rows.  So q, k, v may be
                           slices of one projection output. */

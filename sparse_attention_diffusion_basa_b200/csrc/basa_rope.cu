@@ -39,7 +39,7 @@ struct RopePart {      // one of q, k, v
   int ctas;            // along the tokens
   int chunks;          // CTAs that share a token's heads
   int steps;           // of 512 / d heads each, per chunk
-  float mul;           // e4m3 output: 1 / descale
+  float mul, rest;     // e4m3 output: 1 / factor rounded toward zero, and what is left of it
   float inv;           // 1 / values of a token's row
 };
 
@@ -222,10 +222,28 @@ __device__ __forceinline__ int part_of(const RopeArgs& a, int& chunk, int& cta) 
   return part;
 }
 
+// An e4m3 output is value / factor, rounded to fp32 and then to e4m3.  Where a value
+// has not been scaled before, a product with the factor's reciprocal, itself rounded,
+// does not do: quotients of bf16 values lie at ties of e4m3 (0.75 / 0.03 = 25, between
+// 24 and 26), and 0.75% of v's values went the other way.  With 1 / factor in two
+// terms the quotient is off by at most 2^-46 of itself ahead of its rounding to fp32.
+// `rest` is positive, so that an infinity stays one.  A division took 123 us for the
+// 128 x 128 grid without a norm, this 77, one product 75.  Behind a norm one product
+// is taken into 1 / rms: those values are rounded already and meet a tie by chance
+// alone.
+__device__ __forceinline__ void divide8(f2 (&A)[4], f2 (&B)[4], const RopePart& P) {
+  const f2 m = pk(P.mul, P.mul), rest = pk(P.rest, P.rest);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    A[i] = fma2(A[i], m, mul2(A[i], rest));
+    B[i] = fma2(B[i], m, mul2(B[i], rest));
+  }
+}
+
 // v: rows copied (or narrowed) two heads' worth at a time.
 template <typename TI, typename TO, int kLph, bool kHalves>
 __device__ __forceinline__ void copy_rows(const TI* x, TO* o, const Lane& l, int h0, int hend,
-                                          float mul) {
+                                          const RopePart& P) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16;
   for (int h = h0; h < hend; h += 2 * kHpw) {
     Raw8<TI> ra[2], rb[2];
@@ -240,13 +258,7 @@ __device__ __forceinline__ void copy_rows(const TI* x, TO* o, const Lane& l, int
       if (h + u * kHpw < hend) {
         f2 A[4], B[4];
         unpack16<kHalves>(ra[u], rb[u], A, B);
-        if (sizeof(TO) == 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            A[i] = mul2(A[i], pk(mul, mul));
-            B[i] = mul2(B[i], pk(mul, mul));
-          }
-        }
+        if (sizeof(TO) == 1) divide8(A, B, P);
         pack16<kHalves>(o + (h + u * kHpw) * kD, l, A, B);
       }
   }
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
   const long long dx = (long long)stride * P.ldx, dout = (long long)stride * P.ldo;
   if (part == 2) {
     for (; n < a.tokens; n += stride, x += dx, o += dout)
-      copy_rows<TI, TO, kLph, kHalves>(x, o, l, h0, hend, P.mul);
+      copy_rows<TI, TO, kLph, kHalves>(x, o, l, h0, hend, P);
     return;
   }
   if (n >= a.tokens) return;  // a whole warp; the kernel has no CTA barrier
@@ -397,9 +409,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
       for (int i = 0; i < 4; ++i) {
         const f2 p = fma2(A[i], CA[i], mul2(B[i], SB[i]));
         const f2 q = fma2(B[i], CB[i], mul2(A[i], SA[i]));
-        A[i] = kNorm || sizeof(TO) == 1 ? mul2(p, rr) : p;
-        B[i] = kNorm || sizeof(TO) == 1 ? mul2(q, rr) : q;
+        A[i] = kNorm ? mul2(p, rr) : p;
+        B[i] = kNorm ? mul2(q, rr) : q;
       }
+      if (!kNorm && sizeof(TO) == 1) divide8(A, B, P);
       if (h < hend) pack16<kHalves>(o + h * kD, l, A, B);
     }
   }
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
   const long long dg = (long long)stride * P.ldg, dout = (long long)stride * P.ldo;
   if (part == 2) {
     for (; n < a.tokens; n += stride, g += dg, o += dout)
-      copy_rows<T, T, kLph, kHalves>(g, o, l, h0, hend, 1.f);
+      copy_rows<T, T, kLph, kHalves>(g, o, l, h0, hend, P);
     return;
   }
   const T* x = kNorm ? static_cast<const T*>(P.x) + (long long)n * P.ldx : nullptr;
@@ -745,7 +758,6 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
   };
   const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
   if (part == 2) {
-    const f2 mm = pk(mul, mul);
 #pragma unroll
     for (int s = 0; s < kDepth - 1; ++s) fetch();
     for (; n < a.tokens; n += stride) {
@@ -756,13 +768,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
       for (int j = 0; j < kV; ++j) {
         f2 A[4], B[4];
         take(j, A, B);
-        if (sizeof(TO) == 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            A[i] = mul2(A[i], mm);
-            B[i] = mul2(B[i], mm);
-          }
-        }
+        if (sizeof(TO) == 1) divide8(A, B, P);
         if (on[j]) pack16<kHalves>(o + j * dh, l, A, B);
       }
       from = from + stage == kDepth * stage ? 0 : from + stage;
@@ -1045,6 +1051,8 @@ struct RopeDims {
 };
 
 bool bad_factor(float f) { return !(f >= 0.f) || isinf(f); }
+// Beyond these 1 / factor in two terms would leave fp32's normal numbers.
+bool far_factor(float f) { return f > 0.f && (f < 0x1p-100f || f > 0x1p100f); }
 
 basa_status check_rope(const basa_rope_params* p, bool bwd, RopeDims* r) {
   if (!p) return BASA_ERR_INVALID_ARG;
@@ -1062,6 +1070,9 @@ basa_status check_rope(const basa_rope_params* p, bool bwd, RopeDims* r) {
   if (p->norm != BASA_ROPE_NORM_NONE && (!(p->eps > 0.f) || isinf(p->eps)))
     return BASA_ERR_INVALID_ARG;
   if (bad_factor(p->q_descale) || bad_factor(p->k_descale) || bad_factor(p->v_descale))
+    return BASA_ERR_INVALID_ARG;
+  if (p->out_dtype == BASA_FP8_E4M3 &&
+      (far_factor(p->q_descale) || far_factor(p->k_descale) || far_factor(p->v_descale)))
     return BASA_ERR_INVALID_ARG;
   if (p->at < 0 || p->ah < 0 || p->aw < 0 || ((p->at | p->ah | p->aw) & 1))
     return BASA_ERR_INVALID_ARG;
@@ -1264,7 +1275,12 @@ RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid&
     a.part[i].ldg = row;
     a.part[i].ldo = bwd && gr[i] ? gr[i] : row;
     a.part[i].inv = 1.f / (float)row;
-    a.part[i].mul = 1.f / (ds[i] > 0.f ? ds[i] : 1.f);
+    const double inv = 1.0 / (ds[i] > 0.f ? (double)ds[i] : 1.0);
+    float mul = (float)inv;
+    if ((double)mul > inv) mul = nextafterf(mul, 0.f);
+    const float rest = (float)(inv - (double)mul);
+    a.part[i].mul = mul;
+    a.part[i].rest = rest > 0.f ? rest : 1e-45f;
   }
   return a;
 }

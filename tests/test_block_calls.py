@@ -98,3 +98,20 @@ def test_no_scalar_tensor_is_kept(calls):
     del s
     gc.collect()
     assert kept() is None
+
+
+def test_factors_without_a_reciprocal_are_refused():
+    """An e4m3 factor whose reciprocal leaves fp32's normal numbers: zeros would become NaN."""
+    from sparse_attention_diffusion_basa_b200 import _lib, build
+    build.build()
+    lib, at16 = _lib.load(), 0x10000  # an address that is never used
+    for factor, code in ((1e-45, 1), (1e-39, 1), (7e-31, 1), (1.5e30, 1), (3e38, 1), (8e-31, 4), (1.2e30, 4)):
+        for name in ("q_descale", "k_descale", "v_descale"):
+            p = _lib.BasaRopeParams(1, 2, 2, 1, 8, 8, 64, 0, 0, 0, 0, 0, 1e-6, 1, 2, 1)
+            setattr(p, name, factor)
+            # an unaligned output is found behind the parameters, and ahead of a launch
+            got = lib.basa_qkv_rope(at16, at16, at16, None, None, None, at16, at16, at16 + 8, ctypes.byref(p), None)
+            assert got == code, (name, factor)
+            p.out_dtype = 1  # the factors of a bf16 output are not looked at
+            got = lib.basa_qkv_rope(at16, at16, at16, None, None, None, at16, at16, at16 + 8, ctypes.byref(p), None)
+            assert got == 4, (name, factor)

@@ -47,3 +47,30 @@ def test_scalar_tensors_follow_their_values(basa):
             assert all(equal(a, b) for a, b in zip(got, want))
             got, want = basa.gated_norm(x, y, res_scale=r), basa.gated_norm(x, y, res_scale=res)
             assert all(equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm", [None, "head", "token"])
+def test_e4m3_is_the_rounded_quotient(basa, dtype, norm):
+    """v, and q and k without a norm or angles, are value / factor rounded to fp32 and then to e4m3,
+    at the values of bf16 where ties lie (0.75 / 0.03 = 25, between 24 and 26).  The oracle divides in
+    64 bits: rounding that quotient to 24 bits gives the correctly rounded one, since 53 >= 2 * 24 + 2.
+    So every element has to be equal."""
+    m = torch.arange(128, 256, dtype=torch.float64) / 128           # every significand of bf16
+    vals = torch.cat([s * m * 2.0 ** e for e in range(-12, 5) for s in (1.0, -1.0)])
+    x = vals.to(dtype).cuda().view(1, 1, 1, 34, 1, 128)
+    for factor in (0.03, 0.04, 0.07, 1.0 / 3.0, 3.0, 0.0):
+        f32 = torch.tensor(factor or 1.0, dtype=F32).double()
+        want = (vals.to(dtype).double() / f32).float().clamp(-448.0, 448.0).to(E4).view(x.shape)
+        got = basa.qkv_rope(x, x, x, norm=norm, out_dtype=E4, descale=(factor,) * 3)
+        for name, o in zip("qkv", got):
+            if name == "v" or norm is None:
+                off = (o.cpu().float() != want.float()).sum().item()
+                assert off == 0, f"{name} / {factor}: {off} of {o.numel()} values"
+    far = torch.tensor([float("inf"), -float("inf"), 1e30, -1e30, float("nan"), 0.0, -0.0, 1.0]).to(dtype)
+    x = far.cuda().repeat(16).view(1, 1, 1, 1, 1, 128)
+    for factor in (1e-30, 1e-3, 0.5, 1e30):  # the outermost factors that are taken, nearly
+        _, _, v = basa.qkv_rope(x, x, x, norm=norm, out_dtype=E4, descale=(factor,) * 3)
+        want = (far.float() / torch.tensor(factor, dtype=F32)).clamp(-448.0, 448.0).to(E4).repeat(16)
+        assert equal(v.cpu().view(-1)[:4], want[:4]) and equal(v.cpu().view(-1)[5:8], want[5:8])
+        assert torch.isnan(v.cpu().view(-1)[4].float())
