@@ -620,20 +620,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     copy_commit();
   };
+  const int first_end = ahead_end;
   for (int s = 0; s < a.depth; ++s) fetch(s * stage);
   ColSums<kV> sum;
   int end = r0;
   const long long g_first = g;
   bool flushed = false;
   float4 st_next[kR];
-  auto stats_of = [&](int r) {  // of the rows from r on, ahead of their use
+  // Of the rows from r on, ahead of their use; zeros beside an odd last row of a
+  // modulation (end: of its rows), not the next one's statistics, which may not be
+  // finite and would reach this one's sums as 0 * NaN.
+  auto stats_of = [&](int r, int end) {
 #pragma unroll
     for (int k = 0; k < kR; ++k) {
       st_next[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.st && r + k < r1) st_next[k] = __ldg(a.st + r + k);
+      if (a.st && r + k < (k ? end : r1)) st_next[k] = __ldg(a.st + r + k);
     }
   };
-  stats_of(r0);
+  stats_of(r0, first_end);
   for (int r = r0;;) {
     if (r == end) {
       if (r > r0) {
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       rows += on[k] ? 1 : 0;
       st[k] = st_next[k];
     }
-    stats_of(r + rows);
+    stats_of(r + rows, r + rows < end ? end : (int)min((long long)r1, r + rows + a.group));
     ring_wait(a.depth);
     __syncwarp();  // what the other lanes have copied
     c.first = anew(c.first);

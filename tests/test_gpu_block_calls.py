@@ -74,3 +74,33 @@ def test_e4m3_is_the_rounded_quotient(basa, dtype, norm):
         want = (far.float() / torch.tensor(factor, dtype=F32)).clamp(-448.0, 448.0).to(E4).repeat(16)
         assert equal(v.cpu().view(-1)[:4], want[:4]) and equal(v.cpu().view(-1)[5:8], want[5:8])
         assert torch.isnan(v.cpu().view(-1)[4].float())
+
+
+@pytest.mark.parametrize("lead,mods", [((2, 1), 1), ((4, 5), 1), ((1, 9), 2), ((3, 7), 2), ((2, 333), 1)])
+@pytest.mark.parametrize("C", [256, 5120, 5128])
+@pytest.mark.parametrize("post", [None, "layer"])
+def test_border_gradients_of_a_clean_sample_stay_clean(basa, lead, mods, C, post):
+    """A row that is not finite belongs to one row of modulations: the others' sums, and the rows
+    around it, have the bits of a run without it (odd counts, so that a last row stands alone)."""
+    x, y, gh, gx = (rnd(i, *lead, C) for i in range(4))
+    gate, scale, shift = (rnd(10 + i, *lead[:mods], C) for i in range(3))
+    kw = dict(gate=gate, scale=scale, shift=shift, norm="layer", post_norm=post)
+    _, _, st = basa.gated_norm(x, y, return_stats=True, **kw)
+    clean = basa.gated_norm_bwd(gh, x, st, y, gx, **kw)
+    groups = gate.numel() // C
+    per = x.numel() // C // groups
+    for g in range(groups):
+        for value in (float("inf"), float("nan")):
+            xb, yb, sb = x.clone().view(-1, C), y.clone().view(-1, C), st.clone().view(-1, 4)
+            xb[g * per, 3] = yb[g * per, 5] = value  # its first row
+            sb[g * per] = value
+            got = basa.gated_norm_bwd(gh, xb.view(x.shape), sb.view(st.shape), yb.view(x.shape), gx, **kw)
+            others = [i for i in range(groups) if i != g]
+            for name in ("dgate", "dscale", "dshift"):
+                a, b = getattr(got, name).view(groups, C)[others], getattr(clean, name).view(groups, C)[others]
+                assert equal(a, b), (name, g)
+            rows = [i for i in range(groups * per) if i != g * per]
+            assert equal(got.dx.view(-1, C)[rows], clean.dx.view(-1, C)[rows])
+            assert equal(got.dy.view(-1, C)[rows], clean.dy.view(-1, C)[rows])
+        if g == 3:
+            break
