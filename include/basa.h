@@ -333,7 +333,7 @@ typedef struct basa_rope_params {
   int32_t T, Hg, Wg;   /* grid; L text tokens are the grid (1, 1, L) */
   int32_t d;           /* head dim: 32, 64 or 128 */
   int32_t at, ah, aw;  /* rotated elements of a head per axis: even, together at most d; the
-                          rest of the head is not rotated.  Pairs 0 .. at/2 - 1 turn with the
+                          rest of the head is not rotated (without a norm: copied).  Pairs 0 .. at/2 - 1 turn with the
                           time coordinate, the next ah/2 with the row, the next aw/2 with the
                           column.  BASA_ROPE_HALVES needs at + ah + aw a multiple of 16. */
   int32_t layout;      /* BASA_ROPE_PAIRS or BASA_ROPE_HALVES */

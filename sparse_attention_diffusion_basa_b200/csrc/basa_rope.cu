@@ -206,6 +206,36 @@ __device__ __forceinline__ f2 neg2(f2 v) {
   return pk(-f.x, -f.y);
 }
 
+// Which of a lane's eight pairs are rotated, a bit each.
+template <bool kHalves>
+__device__ __forceinline__ uint32_t rotated(const RopeArgs& a, const Lane& l) {
+  if (kHalves) return l.ja >= 0 ? 0xffu : 0u;
+  const int pairs = a.nt + a.nh + a.nw;
+  auto four = [&](int j) { return (1u << min(max(pairs - j, 0), 4)) - 1u; };
+  return four(l.ja) | four(l.jb) << 4;
+}
+// Without a norm: (A, B) become (A C + B N, B C + A S), or, not rotated, stay what they
+// were.  Their sine of zero would not do that: 0 * infinity makes a NaN of a neighbour,
+// and a zero may lose its sign.  (Under a norm an infinity is its head's loss anyway.)
+template <bool kHalves>
+__device__ __forceinline__ void turn(f2 (&A)[4], f2 (&B)[4], const f2 (&C)[4], const f2 (&S)[4],
+                                     const f2 (&N)[4], uint32_t rot) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 p = fma2(A[i], C[i], mul2(B[i], N[i]));
+    const f2 q = fma2(B[i], C[i], mul2(A[i], S[i]));
+    if (kHalves) {
+      A[i] = rot ? p : A[i];
+      B[i] = rot ? q : B[i];
+    } else {
+      const float2 a0 = un(A[i]), b0 = un(B[i]), a1 = un(p), b1 = un(q);
+      const bool x = rot >> (2 * i) & 1, y = rot >> (2 * i) & 2;
+      A[i] = pk(x ? a1.x : a0.x, y ? a1.y : a0.y);
+      B[i] = pk(x ? b1.x : b0.x, y ? b1.y : b0.y);
+    }
+  }
+}
+
 constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
@@ -367,6 +397,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
   f2 WA[4], WB[4];
   if (kNorm) weight16<kHalves>(P.w, a.w_bf16, 0, l, WA, WB);
   const float mul = sizeof(TO) == 1 ? P.mul : 1.f;
+  const uint32_t rot = kNorm ? 0u : rotated<kHalves>(a, l);
   int from = 0, buf = 0;
   for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
     ang.put(cs[warp][buf], lane, 32);
@@ -404,13 +435,17 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
         }
         r *= rsqrtf(lane_sum<kLph>(sum2(add2(s0, s1))) * (1.f / kD) + a.eps);
       }
-      const f2 rr = pk(r, r);
+      if (!kNorm) {
+        turn<kHalves>(A, B, CA, SA, SB, rot);
+      } else {
+        const f2 rr = pk(r, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 p = fma2(A[i], CA[i], mul2(B[i], SB[i]));
-        const f2 q = fma2(B[i], CB[i], mul2(A[i], SA[i]));
-        A[i] = kNorm ? mul2(p, rr) : p;
-        B[i] = kNorm ? mul2(q, rr) : q;
+        for (int i = 0; i < 4; ++i) {
+          const f2 p = fma2(A[i], CA[i], mul2(B[i], SB[i]));
+          const f2 q = fma2(B[i], CB[i], mul2(A[i], SA[i]));
+          A[i] = mul2(p, rr);
+          B[i] = mul2(q, rr);
+        }
       }
       if (!kNorm && sizeof(TO) == 1) divide8(A, B, P);
       if (h < hend) pack16<kHalves>(o + h * kD, l, A, B);
@@ -422,8 +457,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
 // in a lane's own sixteen columns over all its tokens and heads, then over the
 // CTA, and left as one row of partial sums a CTA.  Four CTAs an SM: 128 registers
 // hold the sums and a step without spills; two 128 x 128 grids with 24 heads 260 us.
+// Without a norm there are no sums: five CTAs, as forward (128 x 128 grid 96 us; four,
+// with the selects of what is not rotated, 100).
 template <typename T, int kLph, bool kHalves, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, 4)
+__global__ void __launch_bounds__(kRopeThreads, kNorm ? 4 : 5)
     rope_head_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kHpw = 32 / kLph, kD = kLph * 16, kDepth = kStages<T>;
   constexpr int kStage = Slot<T>::bytes(kNorm ? 4 : 2, 32);
@@ -481,6 +518,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
   if (kNorm) weight16<kHalves>(P.w, a.w_bf16, 0, l, WA, WB);
 #pragma unroll
   for (int i = 0; i < 4; ++i) accA[i] = accB[i] = pk(0.f, 0.f);
+  const uint32_t rot = kNorm ? 0u : rotated<kHalves>(a, l);
   int from = 0, buf = 0;
   for (; n < a.tokens; n += stride, o += dout, buf ^= 1) {
     ang.put(cs[warp][buf], lane, 32);
@@ -500,10 +538,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
       Slot<T>::take(at, 0, 32, lane, ra);
       Slot<T>::take(at, 1, 32, lane, rb);
       unpack16<kHalves>(ra, rb, A, B);
+      if (kNorm) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // turned back
-        GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
-        GB[i] = fma2(B[i], C[i], mul2(A[i], N[i]));
+        for (int i = 0; i < 4; ++i) {  // turned back
+          GA[i] = fma2(A[i], C[i], mul2(B[i], S[i]));
+          GB[i] = fma2(B[i], C[i], mul2(A[i], N[i]));
+        }
+      } else {
+        turn<kHalves>(A, B, C, N, S, rot);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          GA[i] = A[i];
+          GB[i] = B[i];
+        }
       }
       if (kNorm) {
         Slot<T>::take(at, 2, 32, lane, ra);

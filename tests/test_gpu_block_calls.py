@@ -104,3 +104,38 @@ def test_border_gradients_of_a_clean_sample_stay_clean(basa, lead, mods, C, post
             assert equal(got.dy.view(-1, C)[rows], clean.dy.view(-1, C)[rows])
         if g == 3:
             break
+
+
+def tail_case(layout, d, axes, dtype):
+    """(grid, rotated elements, an element of the rest and, for pairs, its neighbour)."""
+    rot = sum(axes)
+    q = rnd(1, 2, 1, 3, 5, 3, d, dtype=dtype)
+    return (1, 3, 5), rot, q
+
+
+TAILS = [("pairs", 64, (0, 14, 10)), ("pairs", 128, (16, 40, 6)), ("pairs", 32, (0, 0, 2)), ("pairs", 64, (0, 0, 0)),
+         ("halves", 64, (0, 16, 16)), ("halves", 128, (16, 40, 24)), ("halves", 128, (0, 0, 0))]
+
+
+@pytest.mark.parametrize("layout,d,axes", TAILS)
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F32, F32), (BF, E4), (F32, E4)])
+def test_what_is_not_rotated_is_not_touched(basa, layout, d, axes, dtype, out):
+    """Without a norm the rest of a head comes through as it is, signs of zeros too, and an infinity
+    there changes nothing beside it: forward (e4m3 stores the largest value) and backward."""
+    grid, rot, q = tail_case(layout, d, axes, dtype)
+    table = basa.rope_table(grid, axes)
+    clean, _, _ = basa.qkv_rope(q, q, None, table, axes, layout=layout, out_dtype=out)
+    for e in sorted({rot, rot + 1, rot + 4, d - 2, d - 1}):
+        bad = q.clone()
+        bad[1, 0, 2, 3, 1, e] = float("inf")
+        bad[0, 0, 0, 0, 2, e] = float("-inf")
+        bad[0, 0, 1, 1, 0, e] = -0.0
+        got, gotk, _ = basa.qkv_rope(bad, bad, None, table, axes, layout=layout, out_dtype=out)
+        want = clean.clone()
+        want[..., rot:] = bad[..., rot:].float().clamp(-448.0, 448.0).to(E4) if out == E4 else bad[..., rot:]
+        assert equal(got, want) and equal(gotk, want), e
+        if out != E4:
+            dq, dk, _, _, _ = basa.qkv_rope_bwd(bad, bad, None, None, None, table, axes, layout=layout)
+            back, _, _, _, _ = basa.qkv_rope_bwd(q, q, None, None, None, table, axes, layout=layout)
+            back[..., rot:] = bad[..., rot:]
+            assert equal(dq, back) and equal(dk, back), e
