@@ -923,8 +923,6 @@ GnArgs gnorm_args(const basa_gnorm_params* p) {
   return a;
 }
 
-constexpr int kSmem = 224 * 1024;  // of an SM's 228 KB, beside static parts and the CTAs' own 1 KB
-
 template <typename K>
 basa_status go(K kernel, const GnArgs& a, unsigned grid, int threads, int smem, cudaStream_t st) {
   if (!allow_smem(kernel, smem)) return BASA_ERR_CUDA;
@@ -946,10 +944,10 @@ basa_status go_fwd_v(GnArgs a, cudaStream_t st) {
   if (a.teams > most) a.teams = (int)most;
   a.direct = a.group < 4 * a.teams;
   // shared memory: the factors, once or for each team, and a ring for each team
-  const int fit = a.direct ? kSmem / (factors + stage) : (kSmem - factors) / stage;
+  const int fit = a.direct ? kMostSmem / (factors + stage) : (kMostSmem - factors) / stage;
   if (a.teams > fit) a.teams = fit;
   const int held = a.direct ? a.teams * factors : factors;
-  a.depth = (kSmem - held) / (a.teams * stage);
+  a.depth = (kMostSmem - held) / (a.teams * stage);
   if (a.depth > 3) a.depth = 3;
   const int smem = held + a.teams * a.depth * stage, threads = a.teams * per_row;
   if (branch && norm) return go(gnorm_kernel<TX, TY, kV, true, true>, a, grid, threads, smem, st);
@@ -985,7 +983,7 @@ BwdShape bwd_shape(const basa_gnorm_params* p) {
   const int sx = p->x_dtype == BASA_BF16 ? 2 : 4, sy = p->dtype == BASA_BF16 ? 2 : 4;
   const int stage = 2 * s.threads * 8 * 2 * (sx + sy);  // 1 x 2 or 2 x 1 vectors of four rows
   s.per_sm = most / s.threads;
-  if (s.per_sm > kSmem / (s.bytes + stage + 2048)) s.per_sm = kSmem / (s.bytes + stage + 2048);
+  if (s.per_sm > kMostSmem / (s.bytes + stage + 2048)) s.per_sm = kMostSmem / (s.bytes + stage + 2048);
   if (s.per_sm > 8) s.per_sm = 8;
   if (s.per_sm < 1) s.per_sm = 1;
   long long cap = (long long)row_sm_count() * s.per_sm;
@@ -1006,7 +1004,7 @@ basa_status go_bwd_t(GnArgs a, const BwdShape& s, cudaStream_t st) {
   const bool branch = a.dy != nullptr, norm = a.norm != BASA_NORM_NONE;
   const int xb = Part<TX, kV>::bytes(s.threads), yb = Part<TY, kV>::bytes(s.threads);
   const int stage = kR * (xb + (branch ? yb : 0) + (norm ? xb + yb : 0));
-  a.depth = (kSmem / s.per_sm - 2048 - s.bytes) / stage;
+  a.depth = (kMostSmem / s.per_sm - 2048 - s.bytes) / stage;
   a.depth = a.depth > 3 ? 3 : a.depth < 1 ? 1 : a.depth;
   const int smem = s.bytes + a.depth * stage;
   const unsigned grid = (unsigned)s.grid;

@@ -1280,7 +1280,7 @@ bool go_bwd(const basa_rope_params* p, const RopeGrid& g, const RopeArgs& a, cud
   if (p->norm == BASA_ROPE_NORM_TOKEN) {
     const int w = g.teams * (int)sizeof(TokenSmem) + weight_bytes(1, g.threads);
     const int stage = Slot<T>::bytes(4, g.threads);
-    const int depth = w + 2 * stage <= 224 * 1024 ? 2 : 1;  // fp32 rows of over 11 K values: 1
+    const int depth = w + 2 * stage <= kMostSmem ? 2 : 1;  // fp32 rows of over 11 K values: 1
     const int smem = w + depth * stage;
     if (g.threads <= 320)
       return halves ? go_token(rope_token_bwd_kernel<T, 320, 2, true>, g, smem, st, a, depth)

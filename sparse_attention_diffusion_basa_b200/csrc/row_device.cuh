@@ -281,12 +281,17 @@ basa_status launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaS
   return BASA_ERR_CUDA;
 }
 
-// Dynamic shared memory beyond what a kernel may use unasked (48 KB with its
-// static part) has to be allowed.
+// Dynamic shared memory of a CTA at most, of an SM's 228 KB beside static parts and the
+// CTAs' own 1 KB.
+constexpr int kMostSmem = 224 * 1024;
+// Dynamic shared memory beyond what a kernel may use unasked (48 KB with its static
+// part) has to be allowed.  What is allowed belongs to the kernel, not to the launch:
+// always the same, or a call of another host thread with narrower rows could lower
+// it between this and the launch.
 template <typename K>
 bool allow_smem(K kernel, int smem) {
   if (smem <= 32 * 1024 ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) ==
           cudaSuccess)
     return true;
   cudaGetLastError();

@@ -1,6 +1,9 @@
 """The calls around the attention (qkv_rope, gated_norm and their backwards) at values, threads and
 buffers where they could go wrong: ties of the output's rounding, infinities beside what is not
 rotated, rows of another sample, two host threads, workspaces of exactly the size asked for."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -139,3 +142,97 @@ def test_what_is_not_rotated_is_not_touched(basa, layout, d, axes, dtype, out):
             back, _, _, _, _ = basa.qkv_rope_bwd(q, q, None, None, None, table, axes, layout=layout)
             back[..., rot:] = bad[..., rot:]
             assert equal(dq, back) and equal(dk, back), e
+
+
+def raw_calls(basa, C):
+    """The four entries that take shared memory by their width, on one row: no-argument functions that
+    return the library's code.  What they read and write is kept by them."""
+    from sparse_attention_diffusion_basa_b200 import _lib
+    lib, stream = _lib.load(), torch.cuda.Stream()
+    H = C // 128
+    x, y, h, dx, dy, dw = (torch.zeros(1, C, device="cuda") for _ in range(6))
+    st, w = torch.ones(1, 4, device="cuda"), torch.ones(C, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    g = _lib.BasaGnormParams(1, 1, C, 1, 0, 1e-6, 1e-6, 1.0, 0, 0, 0, 0, 0, 0, 0)
+    r = _lib.BasaRopeParams(1, H, H, 1, 1, 1, 128, 0, 0, 0, 0, 2, 1e-6, 0, 0, 0)
+    assert lib.basa_qkv_rope_bwd_workspace_size(ctypes.byref(r)) <= ws.numel()
+    p = {k: t.data_ptr() for k, t in dict(x=x, y=y, h=h, dx=dx, dy=dy, dw=dw, st=st, w=w, ws=ws).items()}
+    keep = (x, y, h, dx, dy, dw, st, w, ws, stream)
+    s, g_, r_ = stream.cuda_stream, ctypes.byref(g), ctypes.byref(r)
+    torch.cuda.synchronize()
+
+    def border(_=keep):
+        return lib.basa_gated_norm(p["x"], p["y"], None, None, None, None, None, None, p["x"], p["h"], None, g_, s)
+
+    def border_bwd(_=keep):
+        return lib.basa_gated_norm_bwd(p["h"], p["x"], p["st"], None, None, None, None, None, None, None, p["dx"],
+                                       p["dy"], None, None, None, None, None, None, None, g_, s)
+
+    def prep(_=keep):
+        return lib.basa_qkv_rope(p["x"], p["y"], None, p["w"], p["w"], None, p["dx"], p["dy"], None, r_, s)
+
+    def prep_bwd(_=keep):
+        return lib.basa_qkv_rope_bwd(p["x"], p["y"], None, p["x"], p["y"], p["w"], p["w"], None, p["dx"], p["dy"],
+                                     None, p["dw"], p["dw"], p["ws"], r_, s)
+    return dict(border=border, border_bwd=border_bwd, prep=prep, prep_bwd=prep_bwd)
+
+
+def run_threads(jobs):
+    """Each job in a thread of its own, all let go at once; what they raised."""
+    failed, start = [], threading.Barrier(len(jobs))
+
+    def work(job):
+        try:
+            start.wait()
+            job()
+        except BaseException as e:  # reported by the test's own thread
+            failed.append(repr(e))
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return failed
+
+
+@pytest.mark.parametrize("widths", [(5120, 4096, 5120, 3840), (8192, 6144, 7168, 8064)])
+@pytest.mark.parametrize("name", ["border", "border_bwd", "prep", "prep_bwd"])
+def test_threads_with_different_widths(basa, name, widths):
+    """One kernel's calls from four threads, each of another width and so of other bytes of shared
+    memory: none may change what another's launch is allowed."""
+    calls = [raw_calls(basa, C)[name] for C in widths]
+
+    def job(call):
+        codes = [call() for _ in range(1500)]
+        assert not any(codes), f"{sum(map(bool, codes))} of {len(codes)} calls refused"
+    failed = run_threads([lambda c=c: job(c) for c in calls])
+    torch.cuda.synchronize()
+    assert not failed, failed
+
+
+def test_threads_on_their_own_streams(basa):
+    """Whole steps from four threads at once have the bits of a step alone."""
+    jobs = []
+    for i, C in enumerate((5120, 1024, 8192, 2048)):
+        x, y, gate = rnd(i, 64, C), rnd(10 + i, 64, C), rnd(20 + i, C)
+        q = rnd(30 + i, 1, 1, 4, 16, C // 128, 128, dtype=BF)
+        w = rnd(40 + i, C, dtype=BF, mean=1.0)
+
+        def step(x=x, y=y, gate=gate, q=q, w=w):
+            xo, h, st = basa.gated_norm(x, y, gate=gate, return_stats=True)
+            g = basa.gated_norm_bwd(h, xo, st, y, gate=gate)
+            a = basa.qkv_rope(q, q, q, norm="token", q_weight=w, k_weight=w)
+            b = basa.qkv_rope_bwd(*a, q, q, norm="token", q_weight=w, k_weight=w)
+            return [t for t in (xo, h, st, *g, *a, *b) if t is not None]
+        want = step()
+
+        def job(step=step, want=want):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    got = step()
+                torch.cuda.current_stream().synchronize()
+                assert all(equal(a, b) for a, b in zip(got, want))
+        jobs.append(job)
+    torch.cuda.synchronize()
+    failed = run_threads(jobs)
+    assert not failed, failed
