@@ -144,7 +144,8 @@ def _row_stride(shape, stride, n, name) -> int:
         if ld is None:
             ld = st
         elif st != expect:
-            raise ValueError(f"the rows of {name} {tuple(shape)} must lie at one stride, got {tuple(stride)}")
+            raise ValueError(f"the rows of {name} {tuple(shape)} must lie at one stride, got {tuple(stride)}: "
+                             "make it contiguous")
         expect = st * size
     return ld
 
@@ -418,7 +419,8 @@ def _gnorm_params(x, y_dtype, mods, weights, norm, post_norm, eps, post_eps, res
             continue
         g, ld = _modulation(m, x, name)
         if groups not in (None, g):
-            raise ValueError("gate, scale and shift must have the same leading dims (expand the shorter)")
+            raise ValueError("gate, scale and shift must have the same leading dims "
+                             "(expand the shorter and make it contiguous)")
         if mod_dtype not in (None, m[2]):
             raise TypeError("gate, scale and shift must share a dtype")
         groups, mod_dtype = g, m[2]

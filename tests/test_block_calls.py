@@ -115,3 +115,18 @@ def test_factors_without_a_reciprocal_are_refused():
             p.out_dtype = 1  # the factors of a bf16 output are not looked at
             got = lib.basa_qkv_rope(at16, at16, at16, None, None, None, at16, at16, at16 + 8, ctypes.byref(p), None)
             assert got == 4, (name, factor)
+
+
+def test_modulations_of_unlike_lengths_follow_the_advice(calls):
+    """gate a sample, scale and shift a frame: what the refusal asks for is then accepted."""
+    x = Stub(2, 6, 64)
+    gate, scale = Stub(2, 64), Stub(2, 3, 64)
+    with pytest.raises(ValueError, match="leading dims") as e:
+        block.gated_norm(x, x, gate=gate, scale=scale)
+    assert "contiguous" in str(e.value)
+    block.gated_norm(x, x, gate=Stub(2, 3, 64), scale=scale)
+    assert calls[-1].groups == 6 and calls[-1].ld_gate == 64
+    block.gated_norm(x, x, gate=Stub(2, 64, stride=(0, 1)), scale=Stub(2, 64))  # one row for all samples
+    assert calls[-1].groups == 2 and calls[-1].ld_gate == 0
+    with pytest.raises(ValueError, match="contiguous"):  # expanded, but rows at two strides
+        block.gated_norm(x, x, gate=Stub(2, 3, 64, stride=(64, 0, 1)), scale=scale)

@@ -236,3 +236,22 @@ def test_threads_on_their_own_streams(basa):
     torch.cuda.synchronize()
     failed = run_threads(jobs)
     assert not failed, failed
+
+
+def test_modulations_expanded_as_advised(basa):
+    """A gate a sample beside a scale a frame, the gate expanded and made contiguous: the formula,
+    and a gradient a frame whose sum over frames is the sample's (fp32 sums of 6 rows each way: 2^-21)."""
+    x, y = rnd(1, 2, 12, 256), rnd(2, 2, 12, 256)
+    gate, scale = rnd(3, 2, 256), rnd(4, 2, 3, 256)
+    wide = gate[:, None].expand(2, 3, 256)
+    with pytest.raises(ValueError, match="contiguous"):
+        basa.gated_norm(x, y, gate=wide, scale=scale)
+    wide = wide.contiguous()
+    xo, h, st = basa.gated_norm(x, y, gate=wide, scale=scale, return_stats=True)
+    want, _ = basa.gated_norm(x, y, gate=gate)
+    assert equal(xo, want)
+    gh = rnd(5, 2, 12, 256)
+    g = basa.gated_norm_bwd(gh, xo, st, y, gate=wide, scale=scale)
+    assert g.dgate.shape == wide.shape
+    t = g.dx.double() * y.double()  # res_scale 1: dx is the gradient of the sum
+    assert ((g.dgate.double().sum(1) - t.sum(1)).abs() <= 2.0 ** -21 * t.abs().sum(1)).all()
