@@ -60,6 +60,18 @@ def _floats(xs):
     return tuple(map(float, xs))
 
 
+def _given(stream, device):
+    """``stream`` as the current one, for tensors on ``device`` (a tensor's, or None: not known here)."""
+    if device is not None and device.type == "cuda" and device != stream.device:
+        raise ValueError(f"stream is one of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _device(*tensors):
+    """The device of the first tensor there is."""
+    return next((t.device for t in tensors if isinstance(getattr(t, "device", None), torch.device)), None)
+
+
 def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -241,7 +253,8 @@ def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(
     Coordinate i of an axis stands at position start + step * i; pair j turns by
     position * theta^(-2j / width).  Keep it while grid and positions stay."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        asked = None if device is None else torch.device(device)
+        with _given(stream, _device(out) or (asked if asked is not None and asked.index is not None else None)):
             return rope_table(grid, axes, theta, start, step, device, out)
     plan = _table_plan(_ints(grid), _ints(axes), _meta(out))
     if out is None:
@@ -293,7 +306,7 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
     ``descale`` (0 = 1), as window_attn takes them.  ``out`` gives the outputs; an
     output may be its own dense input."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, _device(q)):
             return qkv_rope(q, k, v, table, axes, layout=layout, norm=norm, q_weight=q_weight, k_weight=k_weight,
                             eps=eps, out_dtype=out_dtype, descale=descale, out=out)
     outs = None if out is None else tuple(_meta(o) for o in out)
@@ -348,7 +361,7 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
     outputs, q and k its inputs.  ``out`` = (dq, dk, dv) gives the tensors to
     write, which may be slices of one buffer."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, _device(dq_out)):
             return qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table, axes, layout=layout, norm=norm,
                                 q_weight=q_weight, k_weight=k_weight, eps=eps, out=out, workspace=workspace)
     outs = None if out is None else tuple(_meta(o) for o in out)
@@ -485,7 +498,7 @@ def gated_norm(x, y=None, *, gate=None, post_weight=None, weight=None, bias=None
     x), norm None gives x_out alone (h is None).  stats (fp32 [B, ..., 4]) is what
     gated_norm_bwd wants.  ``x_out`` may be x, ``h_out`` may be y."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, _device(x)):
             return gated_norm(x, y, gate=gate, post_weight=post_weight, weight=weight, bias=bias, scale=scale,
                               shift=shift, norm=norm, post_norm=post_norm, eps=eps, post_eps=post_eps,
                               res_scale=res_scale, h_dtype=h_dtype, return_stats=return_stats, x_out=x_out,
@@ -546,7 +559,7 @@ def gated_norm_bwd(dh, x_out, stats, y=None, dx_out=None, *, gate=None, post_wei
     None: dh is None and dx_out is required.  dgate, dscale, dshift have the
     modulations' leading dims, dense."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, _device(x_out, dx_out)):
             return gated_norm_bwd(dh, x_out, stats, y, dx_out, gate=gate, post_weight=post_weight, weight=weight,
                                   bias=bias, scale=scale, shift=shift, norm=norm, post_norm=post_norm,
                                   res_scale=res_scale, workspace=workspace)

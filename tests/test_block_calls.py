@@ -3,6 +3,7 @@ makes of its arguments, on the host: tensors are stood in for by their shapes an
 and the library's entry by a function that records the parameter struct, so nothing is launched."""
 import ctypes
 import gc
+import types
 import weakref
 
 import pytest
@@ -130,3 +131,19 @@ def test_modulations_of_unlike_lengths_follow_the_advice(calls):
     assert calls[-1].groups == 2 and calls[-1].ld_gate == 0
     with pytest.raises(ValueError, match="contiguous"):  # expanded, but rows at two strides
         block.gated_norm(x, x, gate=Stub(2, 3, 64, stride=(64, 0, 1)), scale=scale)
+
+
+def test_stream_of_another_device_is_refused(calls):
+    """The tensors lie on cuda:0, the stream on cuda:1: the call could not run on that stream."""
+    far = types.SimpleNamespace(device=torch.device("cuda", 1))
+    q, x, st = Stub(1, 1, 4, 4, 2, 64), Stub(1, 6, 64), Stub(1, 6, 4, dtype=F32)
+    for call in (lambda: block.qkv_rope(q, q, q, stream=far),
+                 lambda: block.qkv_rope_bwd(q, q, q, q, q, stream=far),
+                 lambda: block.gated_norm(x, x, stream=far),
+                 lambda: block.gated_norm_bwd(x, x, st, x, stream=far),
+                 lambda: block.gated_norm_bwd(None, None, None, x, x, norm=None, stream=far),
+                 lambda: block.rope_table((1, 4, 4), (0, 8, 8), out=Stub(32, 2, dtype=F32), stream=far),
+                 lambda: block.rope_table((1, 4, 4), (0, 8, 8), device="cuda:0", stream=far)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert not calls
