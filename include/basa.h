@@ -333,9 +333,9 @@ typedef struct basa_rope_params {
   int32_t T, Hg, Wg;   /* grid; L text tokens are the grid (1, 1, L) */
   int32_t d;           /* head dim: 32, 64 or 128 */
   int32_t at, ah, aw;  /* rotated elements of a head per axis: even, together at most d; the
-                          rest of the head is not rotated (without a norm: copied).  Pairs 0 .. at/2 - 1 turn with the
-                          time coordinate, the next ah/2 with the row, the next aw/2 with the
-                          column.  BASA_ROPE_HALVES needs at + ah + aw a multiple of 16. */
+                          rest of the head is not rotated (without a norm: copied).  Pairs
+                          0 .. at/2 - 1 turn with the time coordinate, the next ah/2 with the
+                          row, the next aw/2 with the column.  BASA_ROPE_HALVES needs at + ah + aw a multiple of 16. */
   int32_t layout;      /* BASA_ROPE_PAIRS or BASA_ROPE_HALVES */
   int32_t norm;        /* BASA_ROPE_NORM_*; _TOKEN takes H * d up to 16384 */
   float eps;           /* of the norm: positive */
@@ -374,7 +374,7 @@ BASA_API basa_status basa_rope_table(float* table, double theta, const double* s
  * ldv apart; q_out, k_out, v_out dense, as the attention calls take them.
  * Weights may be NULL (ones), v and v_out both NULL, table NULL when nothing is
  * rotated.  An output may be its own input (same address, dense rows, same
- * type); other overlap is not allowed.  One launch.
+ * type); other overlap is refused.  One launch.
  */
 BASA_API basa_status basa_qkv_rope(const void* q, const void* k, const void* v,
                                    const void* q_weight, const void* k_weight, const float* table,
@@ -390,7 +390,7 @@ BASA_API basa_status basa_qkv_rope(const void* q, const void* k, const void* v,
  * and a weight's gradient NULL when it is not wanted.  workspace:
  * basa_qkv_rope_bwd_workspace_size(p) bytes (asked with the device of the call
  * current), 16-byte aligned, needed for the weights' gradients only.  dq may be
- * dq_out (and so on) where the rows are dense.
+ * dq_out (and so on) where the rows are dense; other overlap of an output is refused.
  */
 BASA_API size_t basa_qkv_rope_bwd_workspace_size(const basa_rope_params* p);
 BASA_API basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void* dv_out,
@@ -436,7 +436,7 @@ typedef struct basa_gnorm_params {
  * h is taken from the sum before it is rounded to x_dtype.  stats (may be NULL)
  * receives fp32 [rows, 4]: mean and 1/deviation of the norm, then of the
  * post-norm, zeros where there is none.  x_out may be x, and h may be y; other
- * overlap is not allowed.  One launch.
+ * overlap is refused.  One launch.
  */
 BASA_API basa_status basa_gated_norm(const void* x, const void* y, const void* gate,
                                      const void* post_weight, const void* weight,
@@ -452,7 +452,7 @@ BASA_API basa_status basa_gated_norm(const void* x, const void* y, const void* g
  * dscale, dshift: dense [groups, C]; they, dweight, dbias, dpost_weight [C] are
  * NULL when not wanted.  workspace: basa_gated_norm_bwd_workspace_size(p) bytes
  * (asked with the device of the call current), 16-byte aligned, needed for these
- * sums only.  dx may be dx_out; other overlap is not allowed.
+ * sums only.  dx may be dx_out; other overlap of an output is refused.
  */
 BASA_API size_t basa_gated_norm_bwd_workspace_size(const basa_gnorm_params* p);
 BASA_API basa_status basa_gated_norm_bwd(const void* dh, const void* x_out, const float* stats,

@@ -304,7 +304,7 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
     [B, L, heads, d], grid (1, 1, L)), dense or slices of one projection output.
     ``out_dtype`` torch.float8_e4m3fn writes e4m3 values whose factors are
     ``descale`` (0 = 1), as window_attn takes them.  ``out`` gives the outputs; an
-    output may be its own dense input."""
+    output may be its own dense input; outputs that overlap otherwise are refused."""
     if stream is not None:
         with _given(stream, _device(q)):
             return qkv_rope(q, k, v, table, axes, layout=layout, norm=norm, q_weight=q_weight, k_weight=k_weight,
@@ -359,7 +359,7 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
 
     ``dq_out``, ``dk_out``, ``dv_out`` (or None) are the dense gradients of its
     outputs, q and k its inputs.  ``out`` = (dq, dk, dv) gives the tensors to
-    write, which may be slices of one buffer."""
+    write, which may be slices of one buffer (dq may be dq_out, and so on)."""
     if stream is not None:
         with _given(stream, _device(dq_out)):
             return qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table, axes, layout=layout, norm=norm,

@@ -908,6 +908,23 @@ basa_status check_gnorm(const basa_gnorm_params* p) {
   return BASA_OK;
 }
 
+// Bytes of the border's tensors, and the inputs that its two directions share.
+struct GnBytes {
+  long long x, y, m, w, groups;  // of the rows, of a modulation row, of a weight
+  long long ld[3];
+  explicit GnBytes(const basa_gnorm_params* p) {
+    auto es = [](int t) { return t == BASA_BF16 ? 2LL : 4LL; };
+    x = p->rows * p->C * es(p->x_dtype);
+    y = p->rows * p->C * es(p->dtype);
+    m = p->C * es(p->mod_dtype);
+    w = p->C * es(p->w_dtype);
+    groups = p->groups;
+    const int64_t l[3] = {p->ld_gate, p->ld_scale, p->ld_shift};
+    for (int i = 0; i < 3; ++i) ld[i] = l[i] * es(p->mod_dtype);
+  }
+  void mod(Overlap& o, const void* p, int i) const { o.in(p, ld[i] ? groups : 1, m, ld[i]); }
+};
+
 GnArgs gnorm_args(const basa_gnorm_params* p) {
   GnArgs a;
   memset(&a, 0, sizeof(a));
@@ -1043,6 +1060,20 @@ basa_status basa_gated_norm(const void* x, const void* y, const void* gate, cons
   if (off16(x) || off16(y) || off16(gate) || off16(post_weight) || off16(weight) || off16(bias) ||
       off16(scale) || off16(shift) || off16(x_out) || off16(h) || off16(stats))
     return BASA_ERR_ALIGN;
+  {
+    Overlap o;
+    const GnBytes n(p);
+    o.in(x, n.x);
+    o.in(y, n.y);
+    n.mod(o, gate, 0);
+    n.mod(o, scale, 1);
+    n.mod(o, shift, 2);
+    for (const void* w : {post_weight, weight, bias}) o.in(w, n.w);
+    o.out(x_out, n.x, x);
+    o.out(h, n.y, y);
+    o.out(stats, p->rows * 16);
+    if (o.any()) return BASA_ERR_INVALID_ARG;
+  }
   GnArgs a = gnorm_args(p);
   a.x = x; a.y = y; a.gate = gate; a.pw = post_weight;
   a.w = weight; a.b = bias; a.scale = scale; a.shift = shift;
@@ -1103,6 +1134,24 @@ basa_status basa_gated_norm_bwd(const void* dh, const void* x_out, const float* 
   if ((mods || weights) && !workspace) return BASA_ERR_WORKSPACE;
   if ((mods || weights) && off16(workspace)) return BASA_ERR_ALIGN;
   const BwdShape sh = bwd_shape(p);
+  {
+    Overlap o;
+    const GnBytes n(p);
+    o.in(dx_out, n.x);
+    if (norm) o.in(dh, n.y);
+    if (norm) o.in(x_out, n.x);
+    if (norm || post) o.in(stats, p->rows * 16);
+    if (need_y) o.in(y, n.y);
+    n.mod(o, gate, 0);
+    n.mod(o, scale, 1);
+    for (const void* w : {post_weight, weight, bias}) o.in(w, n.w);
+    o.out(dx, n.x, dx_out);
+    o.out(dy, n.y);
+    for (void* m : {dgate, dscale, dshift}) o.out(m, n.groups * n.m);
+    for (void* w : {dpost_weight, dweight, dbias}) o.out(w, n.w);
+    if (mods || weights) o.out(workspace, (long long)(part_g_bytes(p, sh) + part_w_bytes(p, sh)));
+    if (o.any()) return BASA_ERR_INVALID_ARG;
+  }
   GnArgs a = gnorm_args(p);
   a.x = x_out; a.y = y; a.gate = gate; a.pw = post_weight;
   a.w = weight; a.b = bias; a.scale = scale;

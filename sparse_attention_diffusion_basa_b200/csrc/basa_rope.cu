@@ -1332,6 +1332,29 @@ RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid&
   return a;
 }
 
+int size_of(int dtype) { return dtype == BASA_F32 ? 4 : dtype == BASA_BF16 ? 2 : 1; }
+// q, k, v (or their gradients): rows of tensor i at ld elements, 0 = dense.
+struct RopeRows {
+  long long tokens, row[3], ld[3];  // bytes
+  RopeRows(const basa_rope_params* p, const RopeDims& r, int dtype, int64_t lq, int64_t lk, int64_t lv) {
+    const int64_t l[3] = {lq, lk, lv};
+    tokens = r.tokens;
+    for (int i = 0; i < 3; ++i) {
+      row[i] = (long long)r.heads[i > 0] * p->d * size_of(dtype);
+      ld[i] = l[i] ? l[i] * size_of(dtype) : row[i];
+    }
+  }
+  bool dense(int i) const { return ld[i] == row[i] || tokens == 1; }
+};
+void add_weights(Overlap& o, const basa_rope_params* p, const RopeDims& r, const void* qw, const void* kw,
+                 const void* table, bool out) {
+  const void* w[2] = {qw, kw};
+  for (int i = 0; i < 2; ++i)
+    o.add(w[i], 1, (long long)(p->norm == BASA_ROPE_NORM_TOKEN ? r.heads[i] : 1) * p->d * size_of(p->w_dtype), 0,
+          out, nullptr);
+  if (r.pairs) o.in(table, r.pairs * 8);
+}
+
 basa_status launched() { return cudaGetLastError() == cudaSuccess ? BASA_OK : BASA_ERR_CUDA; }
 
 }  // namespace
@@ -1386,6 +1409,18 @@ basa_status basa_qkv_rope(const void* q, const void* k, const void* v, const voi
   if (off16(q) || off16(k) || off16(v) || off16(q_weight) || off16(k_weight) || off16(table) ||
       off16(q_out) || off16(k_out) || off16(v_out))
     return BASA_ERR_ALIGN;
+  {
+    Overlap o;
+    const RopeRows from(p, r, p->dtype, p->ldq, p->ldk, p->ldv), to(p, r, p->out_dtype, 0, 0, 0);
+    const void *x[3] = {q, k, v}, *y[3] = {q_out, k_out, v_out};
+    for (int i = 0; i < 3; ++i) {
+      o.in(x[i], r.tokens, from.row[i], from.ld[i]);
+      o.out(y[i], r.tokens, to.row[i], to.ld[i],
+            p->out_dtype == p->dtype && from.dense(i) ? x[i] : nullptr);
+    }
+    add_weights(o, p, r, q_weight, k_weight, table, false);
+    if (o.any()) return BASA_ERR_INVALID_ARG;
+  }
   const RopeGrid g = rope_grid(p, r, v != nullptr, false);
   RopeArgs a = rope_args(p, r, g, table, false);
   a.part[0].x = q; a.part[1].x = k; a.part[2].x = v;
@@ -1449,6 +1484,21 @@ basa_status basa_qkv_rope_bwd(const void* dq_out, const void* dk_out, const void
   if (sums && !workspace) return BASA_ERR_WORKSPACE;
   if (sums && off16(workspace)) return BASA_ERR_ALIGN;
   const RopeGrid g = rope_grid(p, r, dv != nullptr, true);
+  {
+    Overlap o;
+    const RopeRows x(p, r, p->dtype, p->ldq, p->ldk, p->ldv), go(p, r, p->dtype, 0, 0, 0),
+        gx(p, r, p->dtype, p->ldgq, p->ldgk, p->ldgv);
+    const void *in[3] = {q, k, nullptr}, *from[3] = {dq_out, dk_out, dv_out}, *to[3] = {dq, dk, dv};
+    for (int i = 0; i < 3; ++i) {
+      if (norm) o.in(in[i], r.tokens, x.row[i], x.ld[i]);
+      o.in(from[i], r.tokens, go.row[i], go.ld[i]);
+      o.out(to[i], r.tokens, gx.row[i], gx.ld[i], gx.dense(i) ? from[i] : nullptr);
+    }
+    add_weights(o, p, r, q_weight, k_weight, table, false);
+    add_weights(o, p, r, dq_weight, dk_weight, nullptr, true);
+    if (sums) o.out(workspace, (long long)(rope_part_bytes(p, r, g, 0) + rope_part_bytes(p, r, g, 1)));
+    if (o.any()) return BASA_ERR_INVALID_ARG;
+  }
   RopeArgs a = rope_args(p, r, g, table, true);
   a.part[0].x = q; a.part[1].x = k;
   a.part[0].g = dq_out; a.part[1].g = dk_out; a.part[2].g = dv_out;

@@ -307,6 +307,60 @@ inline int row_sm_count() {
   }
   return n;
 }
+// Where a call's tensors lie.  An output may take one input's place where the header
+// says so (same address, dense rows, same type); any other byte of an output that
+// another output or an input has too would be read or written by two parts of a launch.
+struct Overlap {
+  struct Rows {
+    unsigned long long at, bytes, row, ld;  // first to last byte, of a row, from row to row
+    bool out;
+    const void* place;  // of an output: the input whose place it may take
+  };
+  Rows all[24];
+  int n = 0;
+  // rows of `row` bytes, ld bytes apart (0 or one row: dense)
+  void add(const void* p, long long rows, long long row, long long ld, bool out, const void* place) {
+    if (!p || rows <= 0 || row <= 0) return;
+    const bool one = rows == 1 || ld == row;
+    const unsigned long long r = rows, w = row, step = one ? w : ld, bytes = (r - 1) * step + w;
+    all[n++] = Rows{(unsigned long long)reinterpret_cast<uintptr_t>(p), bytes, one ? bytes : w,
+                    one ? 0 : step, out, place};
+  }
+  void in(const void* p, long long rows, long long row, long long ld) { add(p, rows, row, ld, false, nullptr); }
+  void in(const void* p, long long bytes) { in(p, 1, bytes, 0); }
+  void out(const void* p, long long rows, long long row, long long ld, const void* place) {
+    add(p, rows, row, ld, true, place);
+  }
+  void out(const void* p, long long bytes, const void* place = nullptr) { out(p, 1, bytes, 0, place); }
+  // Slices of one buffer lie side by side in what the strides have in common.
+  static bool meet(const Rows& a, const Rows& b) {
+    if (a.at + a.bytes <= b.at || b.at + b.bytes <= a.at) return false;
+    unsigned long long g = a.ld, h = b.ld;
+    while (h) {
+      const unsigned long long t = g % h;
+      g = h;
+      h = t;
+    }
+    if (!g) return true;
+    const unsigned long long off = b.at >= a.at ? (b.at - a.at) % g : (g - (a.at - b.at) % g) % g;
+    return off < a.row || off + b.row > g;
+  }
+  bool any() const {
+    for (int i = 0; i < n; ++i) {
+      if (!all[i].out) continue;
+      bool taken = false;  // the place of one input, once
+      for (int j = 0; j < n; ++j) {
+        if (j == i || (all[j].out && j < i) || !meet(all[i], all[j])) continue;
+        const bool own = !all[j].out && !taken && all[i].place &&
+                         all[j].at == (unsigned long long)reinterpret_cast<uintptr_t>(all[i].place) &&
+                         all[i].at == all[j].at && all[i].bytes == all[j].bytes;
+        if (!own) return true;
+        taken = true;
+      }
+    }
+    return false;
+  }
+};
 inline bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 

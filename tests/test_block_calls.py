@@ -147,3 +147,137 @@ def test_stream_of_another_device_is_refused(calls):
         with pytest.raises(ValueError, match="stream"):
             call()
     assert not calls
+
+
+@pytest.fixture
+def codes(calls, monkeypatch):
+    """The library's own answers to calls on made-up addresses, which it must give ahead of a launch:
+    without a device, a call that passes every check ends in BASA_ERR_CUDA."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses are for a machine without a device")
+    seen = []
+
+    def on(device, fn, what, *args):
+        seen.append(fn(*args, None))
+    monkeypatch.setattr(block, "_on", on)
+    return seen
+
+
+PASSED, REFUSED = 6, 1
+
+
+def at(t, byte, **kw):
+    shape = kw.get("shape", t.shape)
+    return Stub(*shape, dtype=kw.get("dtype", t.dtype), stride=kw.get("stride"), at=t.data_ptr() + byte)
+
+
+def test_overlapping_outputs_are_refused(codes):
+    q, k, v = (Stub(1, 1, 4, 4, 2, 64) for _ in range(3))
+    nbytes = 16 * 2 * 64 * 2
+    new = lambda dtype=BF: Stub(*q.shape, dtype=dtype)  # noqa: E731
+    t, table, w = new(), Stub(4 * 32, 2, dtype=F32), Stub(64)
+    axes = (0, 32, 32)
+    f = lambda out, **kw: block.qkv_rope(q, k, v, table, axes, norm="head", q_weight=w, out=out, **kw)  # noqa: E731
+    for out in ((new(), new(), new()), (q, k, v), (t, at(t, nbytes), at(t, 2 * nbytes)), (q, new(), new())):
+        f(out)
+        assert codes[-1] == PASSED
+    for out in ((t, t, new()), (t, new(), t), (new(), t, t), (t, at(t, nbytes - 16), v), (k, q, v), (k, new(), v),
+                (at(q, 16), k, v), (at(q, -16), k, v), (t, v, new()), (at(w, 128 - nbytes, shape=q.shape), k, v),
+                (at(table, 16, shape=q.shape, dtype=BF), k, v)):
+        f(out)
+        assert codes[-1] == REFUSED
+    # in place only where a token's bytes stay where they are
+    f((new(E4), new(E4), new(E4)), out_dtype=E4)
+    assert codes[-1] == PASSED
+    f((at(q, 0, dtype=E4), new(E4), new(E4)), out_dtype=E4)
+    assert codes[-1] == REFUSED
+    # the same tensor as both inputs: neither output can take its place
+    block.qkv_rope(q, q, None, table, axes, out=(new(), new(), None))
+    assert codes[-1] == PASSED
+    block.qkv_rope(q, q, None, table, axes, out=(q, new(), None))
+    assert codes[-1] == REFUSED
+    # slices of one projection: dense outputs may not lie in it, one in a gap between its rows may
+    rows = (16 * 512, 16 * 512, 4 * 512, 512, 64, 1)
+    whole = Stub(*q.shape, stride=rows)
+    x = [at(whole, 256 * i, stride=rows) for i in range(3)]
+    one = Stub(1, 1, 1, 1, 2, 64)
+    block.qkv_rope(*x, table, axes, out=(new(), new(), new()))
+    assert codes[-1] == PASSED
+    block.qkv_rope(*x, table, axes, out=(at(whole, 0), new(), new()))
+    assert codes[-1] == REFUSED
+    block.qkv_rope(x[0], x[1], None, table, axes, out=(at(whole, 768, shape=q.shape), new(), None))
+    assert codes[-1] == REFUSED
+    block.qkv_rope(one, one, None, out=(at(whole, 768, shape=one.shape), at(whole, 1792, shape=one.shape), None))
+    assert codes[-1] == PASSED
+
+
+def test_overlapping_gradients_are_refused(codes):
+    shape = (1, 1, 4, 4, 2, 64)
+    q, k, gq, gk, gv = (Stub(*shape) for _ in range(5))
+    table, axes = Stub(4 * 32, 2, dtype=F32), (0, 32, 32)
+
+    def sliced(ld, *offs):
+        whole = Stub(*shape, stride=(16 * ld, 16 * ld, 4 * ld, ld, 64, 1))
+        return [at(whole, 2 * o, stride=whole.stride()) for o in offs]
+    f = lambda out, **kw: block.qkv_rope_bwd(gq, gk, gv, q, k, table, axes, norm="head", out=out, **kw)  # noqa: E731
+    for out in (sliced(384, 0, 128, 256), sliced(400, 8, 136, 264), sliced(384, 256, 0, 128),
+                sliced(512, 384 + 512 * 16, 128, 256), sliced(384, 0, 384 + 128, 768 + 256), (gq, gk, gv)):
+        f(out)
+        assert codes[-1] == PASSED
+    for out in (sliced(384, 0, 120, 256), sliced(384, 0, 128, 128), sliced(384, 0, 128, 264), (gk, gq, gv),
+                (gq, gq, gv), (q, gk, gv), (Stub(*shape), k, gv), sliced(384, 128, 0, 384 + 8)):
+        f(out)
+        assert codes[-1] == REFUSED
+    # without a norm q and k are not read
+    block.qkv_rope_bwd(gq, gk, gv, q, k, table, axes, out=(q, k, gv))
+    assert codes[-1] == PASSED
+    # rows at different strides that never meet, and that do
+    a = Stub(*shape, stride=(16 * 256, 16 * 256, 4 * 256, 256, 64, 1))
+    wide = (16 * 512, 16 * 512, 4 * 512, 512, 64, 1)
+    f((a, at(a, 2 * 128, stride=wide), Stub(*shape)))
+    assert codes[-1] == PASSED
+    f((a, at(a, 2 * 136, stride=wide), Stub(*shape)))
+    assert codes[-1] == REFUSED
+
+
+def test_overlapping_border_outputs_are_refused(codes):
+    x, y = Stub(2, 6, 64), Stub(2, 6, 64)
+    gate, w, t = Stub(2, 64), Stub(64), Stub(2, 6, 64)
+    nbytes = 2 * 6 * 64 * 2
+    f = lambda **kw: block.gated_norm(x, y, gate=gate, weight=w, **kw)  # noqa: E731
+    for kw in (dict(x_out=x, h_out=y), dict(x_out=x), dict(h_out=y), dict(x_out=t, h_out=at(t, nbytes))):
+        f(**kw)
+        assert codes[-1] == PASSED
+    for kw in (dict(x_out=t, h_out=t), dict(x_out=y), dict(h_out=x), dict(x_out=y, h_out=x), dict(x_out=x, h_out=x),
+               dict(x_out=t, h_out=at(t, nbytes - 16)), dict(x_out=at(x, 16)), dict(h_out=at(y, -16)),
+               dict(h_out=at(gate, 0, shape=x.shape)), dict(h_out=at(gate, 128 - nbytes + 16, shape=x.shape)),
+               dict(x_out=at(w, 16 - nbytes, shape=x.shape))):
+        f(**kw)
+        assert codes[-1] == REFUSED
+    block.gated_norm(x, x, x_out=x)  # the same tensor joins itself: the sum has no place of its own
+    assert codes[-1] == REFUSED
+    block.gated_norm(x, None, h_out=t)
+    assert codes[-1] == PASSED
+    block.gated_norm(x, None, h_out=x)
+    assert codes[-1] == REFUSED
+
+
+def test_overlapping_border_gradients_are_refused(codes):
+    """The C entry, which takes every output from its caller."""
+    from sparse_attention_diffusion_basa_b200 import _lib
+    prm = _lib.BasaGnormParams(12, 3, 64, 1, 2, 1e-6, 1e-6, 1.0, 1, 1, 1, 1, 64, 64, 64)
+    ins = ["gh", "xo", "stats", "y", "gx", "gate", "pw", "w", "b", "scale"]
+    outs = ["dx", "dy", "dgate", "dpw", "dw", "db", "dscale", "dshift", "ws"]
+    base = {name: (i + 1) << 32 for i, name in enumerate(ins + outs)}
+
+    def call(**kw):
+        return _lib.load().basa_gated_norm_bwd(*{**base, **kw}.values(), ctypes.byref(prm), None)
+    assert call() == PASSED and call(dx=base["gx"]) == PASSED
+    for i, name in enumerate(outs):
+        for other in ins + outs[:i]:
+            if (name, other) != ("dx", "gx"):
+                assert call(**{name: base[other]}) == REFUSED, (name, other)
+    assert call(dgate=base["dscale"] + 3 * 64 * 2) == PASSED
+    assert call(dgate=base["dscale"] + 3 * 64 * 2 - 16) == REFUSED
+    need = _lib.load().basa_gated_norm_bwd_workspace_size(ctypes.byref(prm))
+    assert call(dw=base["ws"] + need) == PASSED and call(dw=base["ws"] + need - 256) == REFUSED

@@ -150,14 +150,14 @@ def raw_calls(basa, C):
     from sparse_attention_diffusion_basa_b200 import _lib
     lib, stream = _lib.load(), torch.cuda.Stream()
     H = C // 128
-    x, y, h, dx, dy, dw = (torch.zeros(1, C, device="cuda") for _ in range(6))
+    x, y, h, dx, dy, dq, dk = (torch.zeros(1, C, device="cuda") for _ in range(7))
     st, w = torch.ones(1, 4, device="cuda"), torch.ones(C, device="cuda")
     ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
     g = _lib.BasaGnormParams(1, 1, C, 1, 0, 1e-6, 1e-6, 1.0, 0, 0, 0, 0, 0, 0, 0)
     r = _lib.BasaRopeParams(1, H, H, 1, 1, 1, 128, 0, 0, 0, 0, 2, 1e-6, 0, 0, 0)
     assert lib.basa_qkv_rope_bwd_workspace_size(ctypes.byref(r)) <= ws.numel()
-    p = {k: t.data_ptr() for k, t in dict(x=x, y=y, h=h, dx=dx, dy=dy, dw=dw, st=st, w=w, ws=ws).items()}
-    keep = (x, y, h, dx, dy, dw, st, w, ws, stream)
+    p = {k: t.data_ptr() for k, t in dict(x=x, y=y, h=h, dx=dx, dy=dy, dq=dq, dk=dk, st=st, w=w, ws=ws).items()}
+    keep = (x, y, h, dx, dy, dq, dk, st, w, ws, stream)
     s, g_, r_ = stream.cuda_stream, ctypes.byref(g), ctypes.byref(r)
     torch.cuda.synchronize()
 
@@ -173,7 +173,7 @@ def raw_calls(basa, C):
 
     def prep_bwd(_=keep):
         return lib.basa_qkv_rope_bwd(p["x"], p["y"], None, p["x"], p["y"], p["w"], p["w"], None, p["dx"], p["dy"],
-                                     None, p["dw"], p["dw"], p["ws"], r_, s)
+                                     None, p["dq"], p["dk"], p["ws"], r_, s)
     return dict(border=border, border_bwd=border_bwd, prep=prep, prep_bwd=prep_bwd)
 
 
@@ -255,3 +255,28 @@ def test_modulations_expanded_as_advised(basa):
     assert g.dgate.shape == wide.shape
     t = g.dx.double() * y.double()  # res_scale 1: dx is the gradient of the sum
     assert ((g.dgate.double().sum(1) - t.sum(1)).abs() <= 2.0 ** -21 * t.abs().sum(1)).all()
+
+
+def test_overlapping_outputs_are_refused(basa):
+    """Before a launch: nothing is written.  Slices of one buffer, and an input's own place, are taken."""
+    q, k, v = (rnd(i, 1, 1, 4, 8, 2, 64, dtype=BF) for i in range(3))
+    t, u = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    for out in ((t, t, u), (t, u, t), (k, q, u), (t, u, q), (t, t.view(-1).view_as(q), u)):
+        with pytest.raises(basa.BasaError, match="INVALID_ARG"):
+            basa.qkv_rope(q, k, v, out=out)
+        with pytest.raises(basa.BasaError, match="INVALID_ARG"):
+            basa.qkv_rope_bwd(q, k, v, None, None, out=out)
+    x, y = q.view(1, 32, 128), k.view(1, 32, 128)
+    a = t.view(1, 32, 128)
+    for kw in (dict(x_out=a, h_out=a), dict(x_out=y), dict(h_out=x), dict(x_out=x, h_out=x)):
+        with pytest.raises(basa.BasaError, match="INVALID_ARG"):
+            basa.gated_norm(x, y, **kw)
+    torch.cuda.synchronize()
+    assert (t == 7.0).all() and (u == 7.0).all()
+    whole = torch.empty(1, 1, 4, 8, 6, 64, dtype=BF, device="cuda")
+    want = basa.qkv_rope_bwd(q, k, v, None, None)
+    got = basa.qkv_rope_bwd(q, k, v, None, None, out=whole.split(2, -2))
+    assert all(equal(g, w) for g, w in zip(got, want))
+    want, got = basa.gated_norm(x, y), basa.gated_norm(x, y, x_out=x, h_out=y)
+    assert got[0] is x and got[1] is y
+    assert all(equal(g, w) for g, w in zip(got, want))
