@@ -60,6 +60,12 @@ def _floats(xs):
     return tuple(map(float, xs))
 
 
+def _three(xs, name):
+    if len(xs) != 3:
+        raise ValueError(f"{name} must give three values, got {xs}")
+    return xs
+
+
 def _given(stream, device):
     """``stream`` as the current one, for tensors on ``device`` (a tensor's, or None: not known here)."""
     if device is not None and device.type == "cuda" and device != stream.device:
@@ -196,7 +202,7 @@ def _rope_params(q, k, axes, layout, norm, eps, out_dtype, descale, lds, w_dtype
     at, ah, aw = axes
     return BasaRopeParams(q[0], H, Hkv, T, Hg, Wg, q[-1], at, ah, aw, _code(BASA_ROPE_LAYOUT, layout, "layout"),
                           _code(BASA_ROPE_NORM, norm, "norm"), eps, _DT[dtype], _DT[out_dtype],
-                          _DT[w_dtype], *descale, *lds)
+                          _DT[w_dtype], *_three(descale, "descale"), *lds)
 
 
 def _pairs(prm) -> int:
@@ -263,6 +269,7 @@ def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(
             raise ValueError("device must be a CUDA device")
         out = torch.empty((plan.pairs, 2), dtype=torch.float32, device=dev)
     d3 = ctypes.c_double * 3
+    start, step = _three(_floats(start), "start"), _three(_floats(step), "step")
     _on(out.device, _lib.load().basa_rope_table, "basa_rope_table", out.data_ptr(), float(theta), d3(*start),
         d3(*step), plan.params)
     return out

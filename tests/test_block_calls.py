@@ -281,3 +281,20 @@ def test_overlapping_border_gradients_are_refused(codes):
     assert call(dgate=base["dscale"] + 3 * 64 * 2 - 16) == REFUSED
     need = _lib.load().basa_gated_norm_bwd_workspace_size(ctypes.byref(prm))
     assert call(dw=base["ws"] + need) == PASSED and call(dw=base["ws"] + need - 256) == REFUSED
+
+
+def test_positions_and_factors_come_in_threes(calls):
+    """start and step give one value an axis, descale one of q, k, v; a missing one is not taken for
+    zero (or for a row stride, which lies behind the factors in the struct)."""
+    out = Stub(32, 2, dtype=F32)
+    block.rope_table((1, 4, 4), (0, 8, 8), start=(0, 1, 2), step=[1, 1, 0.5], out=out)
+    assert len(calls) == 1
+    for kw in (dict(start=(1.0, 2.0)), dict(step=(1.0, 1.0)), dict(start=()), dict(step=(1.0,) * 4)):
+        with pytest.raises(ValueError, match="three"):
+            block.rope_table((1, 4, 4), (0, 8, 8), out=out, **kw)
+    assert len(calls) == 1
+    q = Stub(1, 1, 4, 4, 2, 64)
+    for descale in ((0.5,), (0.5, 0.5), (0.5,) * 4):
+        with pytest.raises(ValueError, match="three"):
+            block.qkv_rope(q, q, q, out_dtype=E4, descale=descale)
+    assert len(calls) == 1
