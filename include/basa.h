@@ -329,7 +329,8 @@ BASA_API basa_status basa_window_attn_noalloc(const void* q, const void* k, cons
 #define BASA_ROPE_NORM_TOKEN 2 /* over all heads of a token; weights [H * d], [Hkv * d] */
 
 typedef struct basa_rope_params {
-  int32_t B, H, Hkv;   /* batch, query heads, K/V heads (0 selects H; H a multiple of Hkv) */
+  int32_t B, H, Hkv;   /* batch, query heads, K/V heads (0 selects H; H a multiple of Hkv,
+                          not 0 beside it) */
   int32_t T, Hg, Wg;   /* grid; L text tokens are the grid (1, 1, L) */
   int32_t d;           /* head dim: 32, 64 or 128 */
   int32_t at, ah, aw;  /* rotated elements of a head per axis: even, together at most d; the

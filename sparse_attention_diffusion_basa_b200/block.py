@@ -196,7 +196,7 @@ def _rope_params(q, k, axes, layout, norm, eps, out_dtype, descale, lds, w_dtype
     if k[:-2] != q[:-2] or k[-1] != q[-1]:
         raise ValueError(f"k {tuple(k)} must match q {tuple(q)} except in heads")
     H, Hkv = q[-2], k[-2]
-    if H != Hkv and (Hkv == 0 or H % Hkv):
+    if H != Hkv and (H == 0 or Hkv == 0 or H % Hkv):
         raise ValueError(f"q heads {H} must be a multiple of k/v heads {Hkv}")
     T, Hg, Wg = q[1:4] if len(q) == 6 else (1, 1, q[1])
     at, ah, aw = axes

@@ -1105,7 +1105,7 @@ basa_status check_rope(const basa_rope_params* p, bool bwd, RopeDims* r) {
   if (!p) return BASA_ERR_INVALID_ARG;
   if (p->B < 0 || p->T < 0 || p->Hg < 0 || p->Wg < 0 || p->H < 0 || p->d <= 0)
     return BASA_ERR_INVALID_ARG;
-  if (p->Hkv < 0 || (p->Hkv > 0 && p->H % p->Hkv != 0)) return BASA_ERR_INVALID_ARG;
+  if (p->Hkv < 0 || (p->Hkv > 0 && (p->H == 0 || p->H % p->Hkv != 0))) return BASA_ERR_INVALID_ARG;
   if (p->dtype != BASA_F32 && p->dtype != BASA_BF16)
     return p->dtype == BASA_FP8_E4M3 ? BASA_ERR_UNSUPPORTED : BASA_ERR_INVALID_ARG;
   if (p->out_dtype != p->dtype && (p->out_dtype != BASA_FP8_E4M3 || bwd))

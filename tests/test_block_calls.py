@@ -298,3 +298,22 @@ def test_positions_and_factors_come_in_threes(calls):
         with pytest.raises(ValueError, match="three"):
             block.qkv_rope(q, q, q, out_dtype=E4, descale=descale)
     assert len(calls) == 1
+
+
+def test_no_query_heads_beside_key_heads_is_refused():
+    """Zero query heads with K/V heads: a call that would leave k's and v's outputs unwritten."""
+    from sparse_attention_diffusion_basa_b200 import _lib, build
+    build.build()
+    lib, at16 = _lib.load(), 0x10000  # an address that is never used
+    for norm in (0, 1, 2):
+        p = _lib.BasaRopeParams(1, 0, 2, 1, 8, 8, 64, 0, 32, 32, 0, norm, 1e-6, 1, 1, 1)
+        w = at16 if norm else None
+        args = [at16] * 3 + [w, w] + [at16] * 4
+        assert lib.basa_qkv_rope(*args, ctypes.byref(p), None) == 1
+        args = [at16] * 5 + [w, w] + [at16] * 4 + [w, w, at16]
+        assert lib.basa_qkv_rope_bwd(*args, ctypes.byref(p), None) == 1
+    q, k = Stub(1, 1, 8, 8, 0, 64), Stub(1, 1, 8, 8, 2, 64)
+    with pytest.raises(ValueError, match="heads"):
+        block.qkv_rope(q, k, k)
+    with pytest.raises(ValueError, match="heads"):
+        block.qkv_rope_bwd(q, k, k, q, k)
