@@ -426,6 +426,8 @@ def _modulation(m, x, name):
     if n and lead != tuple(xs[:n]) and not (
             n == 2 and len(xs) == 3 and lead[0] == xs[0] and lead[1] and xs[1] % lead[1] == 0):
         raise ValueError(f"{name} {tuple(shape)} must be [C], or lead with dims of x {tuple(xs)}")
+    if _numel(lead) == 0:
+        return 0, 0
     return _numel(lead), _row_stride(shape, stride, n, name) or 0
 
 

@@ -317,3 +317,15 @@ def test_no_query_heads_beside_key_heads_is_refused():
         block.qkv_rope(q, k, k)
     with pytest.raises(ValueError, match="heads"):
         block.qkv_rope_bwd(q, k, k, q, k)
+
+
+def test_no_tokens_with_a_modulation_each(calls, monkeypatch):
+    """An empty batch's modulations, one for each of its tokens: an empty call, as with one a sample."""
+    monkeypatch.setattr(block, "_size", lambda *a: 0)
+    for lead in ((2, 0), (0, 3), (0, 0)):
+        x, st = Stub(*lead, 64), Stub(*lead, 4, dtype=F32)
+        m = Stub(*lead, 64)
+        block.gated_norm(x, x, gate=m, scale=m, shift=m)
+        assert calls[-1].rows == 0
+        block.gated_norm_bwd(x, x, st, x, gate=m, scale=m, shift=m)
+        assert calls[-1].rows == 0

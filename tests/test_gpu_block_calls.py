@@ -280,3 +280,13 @@ def test_overlapping_outputs_are_refused(basa):
     want, got = basa.gated_norm(x, y), basa.gated_norm(x, y, x_out=x, h_out=y)
     assert got[0] is x and got[1] is y
     assert all(equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("lead", [(2, 0), (0, 3), (0, 0)])
+def test_no_tokens_with_a_modulation_each(basa, lead):
+    x, m = torch.empty(*lead, 64, device="cuda"), torch.empty(*lead, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    xo, h, st = basa.gated_norm(x, x, gate=m, scale=m, shift=m, weight=w, return_stats=True)
+    assert xo.shape == h.shape == x.shape and st.shape == (*lead, 4)
+    g = basa.gated_norm_bwd(x, xo, st, x, x, gate=m, scale=m, shift=m, weight=w)
+    assert g.dgate.shape == g.dscale.shape == g.dshift.shape == m.shape and (g.dweight == 0).all()
