@@ -329,3 +329,32 @@ def test_no_tokens_with_a_modulation_each(calls, monkeypatch):
         assert calls[-1].rows == 0
         block.gated_norm_bwd(x, x, st, x, gate=m, scale=m, shift=m)
         assert calls[-1].rows == 0
+
+
+def test_workspaces_grow_with_what_they_hold():
+    """At least one partial row of fp32 sums of each kind, and with more tokens or columns more; whole
+    steps of 256 bytes.  (That a call keeps to the size is for a device to show.)"""
+    from sparse_attention_diffusion_basa_b200 import _lib, build
+    build.build()
+    lib = _lib.load()
+
+    def rope(norm, H, Hkv, d, tokens):
+        p = _lib.BasaRopeParams(1, H, Hkv, 1, 1, tokens, d, 0, 0, 0, 0, norm, 1e-6, 1, 1, 1)
+        n = lib.basa_qkv_rope_bwd_workspace_size(ctypes.byref(p))
+        # one row at least of q's and of k's weights
+        assert n % 256 == 0 and n >= 4 * d * (H + Hkv if norm == 2 else 2), (norm, H, Hkv, d, tokens, n)
+        return n
+
+    def border(rows, groups, C):
+        p = _lib.BasaGnormParams(rows, groups, C, 1, 2, 1e-6, 1e-6, 1.0, 1, 1, 1, 1, C, C, C)
+        n = lib.basa_gated_norm_bwd_workspace_size(ctypes.byref(p))
+        assert n % 256 == 0 and n >= 9 * 4 * C  # of one CTA: two modulations' three sums, three of the weights
+        return n
+    for norm in (1, 2):
+        for H, Hkv, d in ((1, 1, 32), (12, 4, 128), (40, 40, 128), (128, 2, 128), (8, 8, 64)):
+            sizes = [rope(norm, H, Hkv, d, t) for t in (1, 7, 100, 1000, 30000)]
+            assert sizes[0] <= sizes[1] < sizes[-1], (norm, H, Hkv, d, sizes)
+    for C in (8, 264, 5120, 8192):
+        sizes = [border(r, 1, C) for r in (1, 4, 100, 3000, 100000)]
+        assert sizes[0] <= sizes[1] < sizes[-1], (C, sizes)
+    assert border(100, 1, 512) > border(100, 1, 256)

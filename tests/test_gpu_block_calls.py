@@ -290,3 +290,82 @@ def test_no_tokens_with_a_modulation_each(basa, lead):
     assert xo.shape == h.shape == x.shape and st.shape == (*lead, 4)
     g = basa.gated_norm_bwd(x, xo, st, x, x, gate=m, scale=m, shift=m, weight=w)
     assert g.dgate.shape == g.dscale.shape == g.dshift.shape == m.shape and (g.dweight == 0).all()
+
+
+GUARD = 1 << 16
+
+
+def guarded(n):
+    """n bytes of 0xff (NaN to whoever reads them unwritten) and a guard behind them."""
+    buf = torch.full((n + GUARD,), 0xff, dtype=torch.uint8, device="cuda")
+    buf[n:] = 0xa5
+    return buf
+
+
+@pytest.mark.parametrize("with_v", [True, False])
+@pytest.mark.parametrize("norm,grid,H,Hkv,d", [
+    ("token", (1, 1, 1), 4, 1, 32), ("token", (2, 9, 31), 12, 1, 128), ("token", (1, 40, 60), 8, 8, 64),
+    ("token", (1, 37, 41), 2, 1, 32), ("token", (1, 30, 50), 40, 8, 128), ("token", (1, 9, 11), 128, 2, 128),
+    ("head", (1, 1, 1), 3, 1, 64), ("head", (1, 64, 65), 24, 8, 128), ("head", (1, 17, 19), 200, 4, 32)])
+def test_preparation_backward_keeps_to_its_workspace(basa, norm, grid, H, Hkv, d, with_v):
+    """A workspace of exactly the bytes asked for, unwritten before: nothing behind it is touched,
+    and the sums are those of the binding's own call and of 64 bits."""
+    lead = (1, *grid)
+    q, gq = rnd(1, *lead, H, d, dtype=BF), rnd(2, *lead, H, d, dtype=BF)
+    k, gk, gv = (rnd(3 + i, *lead, Hkv, d, dtype=BF) for i in range(3))
+    gv = gv if with_v else None
+    n = (d, d) if norm == "head" else (H * d, Hkv * d)
+    qw, kw = (rnd(7 + i, m, mean=1.0, std=0.3) for i, m in enumerate(n))
+    from sparse_attention_diffusion_basa_b200 import _lib
+    prm = _lib.BasaRopeParams(1, H, Hkv, *grid, d, 0, 0, 0, 0, _lib.BASA_ROPE_NORM[norm], 1e-6, 1, 1, 0)
+    need = _lib.load().basa_qkv_rope_bwd_workspace_size(ctypes.byref(prm))
+    assert need > 0
+    buf = guarded(need)
+    args = (gq, gk, gv, q, k)
+    kw_ = dict(norm=norm, q_weight=qw, k_weight=kw)
+    got = basa.qkv_rope_bwd(*args, workspace=buf[:need], **kw_)
+    torch.cuda.synchronize()
+    assert (buf[need:] == 0xa5).all()
+    with pytest.raises(ValueError, match="workspace"):
+        basa.qkv_rope_bwd(*args, workspace=buf[:need - 1], **kw_)
+    assert all(equal(a, b) for a, b in zip(got, basa.qkv_rope_bwd(*args, **kw_)))
+    dims = (-1,) if norm == "head" else (-2, -1)
+    for x, g, w, dw in ((q, gq, qw, got[3]), (k, gk, kw, got[4])):
+        x64, g64 = x.double(), g.double()
+        r = 1 / torch.sqrt(x64.square().mean(dims, keepdim=True) + 1e-6)
+        t = g64 * x64 * r
+        over = (0, 1, 2, 3, 4) if norm == "head" else (0, 1, 2, 3)
+        # a thread adds fewer than 64 terms, 128 chains add fewer than 32 rows each and are joined in 12
+        # steps; 66 roundings stand around a term
+        assert ((dw.double() - t.sum(over).reshape(-1)).abs()
+                <= 174 * 2.0 ** -24 * t.abs().sum(over).reshape(-1)).all()
+
+
+@pytest.mark.parametrize("rows,groups,C", [(1, 1, 8), (5, 5, 264), (333, 3, 1000), (6000, 1, 256), (6000, 3000, 64),
+                                           (700, 700, 5120), (77, 7, 8192), (4001, 1, 5128)])
+def test_border_backward_keeps_to_its_workspace(basa, rows, groups, C):
+    """The same of the border, with more and with fewer modulation rows than CTAs."""
+    per = rows // groups
+    x, y, gh, gx = (rnd(i, groups, per, C, dtype=BF) for i in range(4))
+    mods, w = [rnd(10 + i, groups, C) for i in range(3)], [rnd(20 + i, C, dtype=BF, mean=1.0) for i in range(3)]
+    kw = dict(gate=mods[0], scale=mods[1], shift=mods[2], post_weight=w[0], weight=w[1], bias=w[2], norm="layer",
+              post_norm="rms")
+    _, _, st = basa.gated_norm(x, y, return_stats=True, **kw)
+    from sparse_attention_diffusion_basa_b200 import _lib
+    prm = _lib.BasaGnormParams(rows, groups, C, 1, 2, 1e-6, 1e-6, 1.0, 1, 1, 0, 1, C, C, C)
+    need = _lib.load().basa_gated_norm_bwd_workspace_size(ctypes.byref(prm))
+    assert need > 0
+    buf = guarded(need)
+    got = basa.gated_norm_bwd(gh, x, st, y, gx, workspace=buf[:need], **kw)
+    torch.cuda.synchronize()
+    assert (buf[need:] == 0xa5).all()
+    with pytest.raises(ValueError, match="workspace"):
+        basa.gated_norm_bwd(gh, x, st, y, gx, workspace=buf[:need - 1], **kw)
+    assert all(equal(a, b) for a, b in zip(got, basa.gated_norm_bwd(gh, x, st, y, gx, **kw)))
+    # shift's and bias's gradients are plain sums: a thread adds fewer than 64 rows, 1184 partial rows
+    # or fewer are added in 32 chains of 37 and joined in 32; a rounding to bf16 for bias
+    t = gh.double()
+    assert ((got.dshift.double() - t.sum(1)).abs() <= 136 * 2.0 ** -24 * t.abs().sum(1)).all()
+    t = t * (1 + mods[1].double()[:, None])
+    ref, tol = t.sum((0, 1)), 140 * 2.0 ** -24 * t.abs().sum((0, 1))
+    assert ((got.dbias.double() - ref).abs() <= tol + (ref.abs() + tol) * 2.0 ** -8).all()
