@@ -52,18 +52,15 @@ def _code(table, key, name):
         raise ValueError(f"{name} must be one of {sorted(map(str, table))}, got {key!r}") from None
 
 
-def _ints(xs):
-    return tuple(map(int, xs))
-
-
-def _floats(xs):
-    return tuple(map(float, xs))
-
-
-def _three(xs, name):
-    if len(xs) != 3:
-        raise ValueError(f"{name} must give three values, got {xs}")
-    return xs
+def _three(xs, name, kind):
+    """Three numbers as Python numbers of ``kind``."""
+    try:
+        a, b, c = xs
+    except ValueError:
+        raise ValueError(f"{name} must give three values, got {xs}") from None
+    if type(a) is kind and type(b) is kind and type(c) is kind:
+        return a, b, c
+    return kind(a), kind(b), kind(c)
 
 
 def _given(stream, device):
@@ -202,7 +199,7 @@ def _rope_params(q, k, axes, layout, norm, eps, out_dtype, descale, lds, w_dtype
     at, ah, aw = axes
     return BasaRopeParams(q[0], H, Hkv, T, Hg, Wg, q[-1], at, ah, aw, _code(BASA_ROPE_LAYOUT, layout, "layout"),
                           _code(BASA_ROPE_NORM, norm, "norm"), eps, _DT[dtype], _DT[out_dtype],
-                          _DT[w_dtype], *_three(descale, "descale"), *lds)
+                          _DT[w_dtype], *descale, *lds)
 
 
 def _pairs(prm) -> int:
@@ -262,16 +259,15 @@ def rope_table(grid, axes, theta: float = 10000.0, start=(0.0, 0.0, 0.0), step=(
         asked = None if device is None else torch.device(device)
         with _given(stream, _device(out) or (asked if asked is not None and asked.index is not None else None)):
             return rope_table(grid, axes, theta, start, step, device, out)
-    plan = _table_plan(_ints(grid), _ints(axes), _meta(out))
+    plan = _table_plan(_three(grid, "grid", int), _three(axes, "axes", int), _meta(out))
     if out is None:
         dev = torch.device("cuda" if device is None else device)
         if dev.type != "cuda":
             raise ValueError("device must be a CUDA device")
         out = torch.empty((plan.pairs, 2), dtype=torch.float32, device=dev)
     d3 = ctypes.c_double * 3
-    start, step = _three(_floats(start), "start"), _three(_floats(step), "step")
-    _on(out.device, _lib.load().basa_rope_table, "basa_rope_table", out.data_ptr(), float(theta), d3(*start),
-        d3(*step), plan.params)
+    _on(out.device, _lib.load().basa_rope_table, "basa_rope_table", out.data_ptr(), float(theta),
+        d3(*_three(start, "start", float)), d3(*_three(step, "step", float)), plan.params)
     return out
 
 
@@ -318,7 +314,8 @@ def qkv_rope(q, k, v=None, table=None, axes=(0, 0, 0), *, layout="pairs", norm=N
                             eps=eps, out_dtype=out_dtype, descale=descale, out=out)
     outs = None if out is None else tuple(_meta(o) for o in out)
     plan = _rope_plan(_meta(q), _meta(k), _meta(v), _meta(q_weight), _meta(k_weight), _meta(table), outs,
-                      _ints(axes), layout, norm, float(eps), out_dtype, _floats(descale))
+                      _three(axes, "axes", int), layout, norm, float(eps), out_dtype,
+                      _three(descale, "descale", float))
     dev = q.device
     if out is None:
         dt = plan.dtype
@@ -373,7 +370,7 @@ def qkv_rope_bwd(dq_out, dk_out, dv_out, q, k, table=None, axes=(0, 0, 0), *, la
                                 q_weight=q_weight, k_weight=k_weight, eps=eps, out=out, workspace=workspace)
     outs = None if out is None else tuple(_meta(o) for o in out)
     plan = _rope_bwd_plan(_meta(dq_out), _meta(dk_out), _meta(dv_out), _meta(q), _meta(k), _meta(q_weight),
-                          _meta(k_weight), _meta(table), outs, _ints(axes), layout, norm, float(eps))
+                          _meta(k_weight), _meta(table), outs, _three(axes, "axes", int), layout, norm, float(eps))
     dev = dq_out.device
     if out is None:
         dq, dk, dv = _like(dq_out), _like(dk_out), None if dv_out is None else _like(dv_out)
