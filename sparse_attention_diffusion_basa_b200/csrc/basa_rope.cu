@@ -40,6 +40,7 @@ struct RopePart {      // one of q, k, v
   int chunks;          // CTAs that share a token's heads
   int steps;           // of 512 / d heads each, per chunk
   float mul, rest;     // e4m3 output: 1 / factor rounded toward zero, and what is left of it
+                       // (q and k behind a norm: mul alone, rounded to nearest)
   float inv;           // 1 / values of a token's row
 };
 
@@ -1324,7 +1325,8 @@ RopeArgs rope_args(const basa_rope_params* p, const RopeDims& r, const RopeGrid&
     a.part[i].inv = 1.f / (float)row;
     const double inv = 1.0 / (ds[i] > 0.f ? (double)ds[i] : 1.0);
     float mul = (float)inv;
-    if ((double)mul > inv) mul = nextafterf(mul, 0.f);
+    const bool two_terms = i == 2 || p->norm == BASA_ROPE_NORM_NONE;
+    if (two_terms && (double)mul > inv) mul = nextafterf(mul, 0.f);
     const float rest = (float)(inv - (double)mul);
     a.part[i].mul = mul;
     a.part[i].rest = rest > 0.f ? rest : 1e-45f;
