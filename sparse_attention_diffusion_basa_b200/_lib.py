@@ -5,8 +5,8 @@ import ctypes
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-# BASA_LIBRARY=checked selects the build whose kernels check every box and
-# output index (python -m sparse_attention_diffusion_basa_b200.build --checked).
+# BASA_LIBRARY=checked selects the build whose attention kernels on the tensor cores
+# check every box and output index (python -m sparse_attention_diffusion_basa_b200.build --checked).
 LIB_PATH = os.path.join(HERE, "_lib", "libbasa_checked.so" if os.environ.get("BASA_LIBRARY") == "checked"
                         else "libbasa.so")
 

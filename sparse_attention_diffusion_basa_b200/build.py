@@ -4,9 +4,9 @@ Usage: ``python -m sparse_attention_diffusion_basa_b200.build [--force] [--verbo
 [--checked]``.  The library links the CUDA runtime statically and resolves the
 TMA map encoder through the driver entry point, so it loads on machines without
 a GPU.  ``--checked`` builds ``_lib/libbasa_checked.so`` instead: the same
-library compiled with BASA_CHECKED, whose kernels check every TMA box and every
-output index against their tensors, skip an access that is out of range and
-report it through the device status word (BASA_ERR_CHECK); the binding loads it
+library compiled with BASA_CHECKED, whose tensor-core attention kernels check every
+TMA box and every output index against their tensors, skip an access that is out of
+range and report it through the device status word (BASA_ERR_CHECK); the binding loads it
 when the environment variable BASA_LIBRARY is ``checked``.
 """
 from __future__ import annotations

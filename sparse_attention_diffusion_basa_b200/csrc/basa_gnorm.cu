@@ -17,10 +17,12 @@
 // thread the same columns of every row; a CTA's rows are a contiguous range, so a
 // modulation row's factors are formed once for many rows, and rows are read ahead
 // by asynchronous copies.  Measured on a B200 (copy 6.57 TB/s), device time of the
-// call: 75600 rows of 5120, fp32 stream and bf16 branch 791 us = 5.87 TB/s (89% of
-// the copy rate; the first form, unpacked and one row at a time, 1172); 14508 rows
-// of 1536 bf16, both norms, a modulation a frame 42 us (65%; about 8 us of it start
-// and end); backward of 16384 rows of 5120 bf16 190 us = 5.30 TB/s (81%; 273).
+// call: 75600 rows of 5120, fp32 stream and bf16 branch 787 to 801 us = 5.80 to 5.90
+// TB/s (88 to 90% of the copy rate; the first form, unpacked and one row at a time,
+// 1172); 14508 rows of 1536 bf16, both norms, a modulation a frame 40 us (68%; about
+// 8 us of it start and end); backward of 16384 rows of 5120 bf16 188 us = 5.36 TB/s
+// (82%; 273).  A modulation a token is far from that (16384 rows of 5120 bf16: 477 us
+// for 179 us of bytes): each team's own factors pass through shared memory.
 #include <math.h>
 #include <string.h>
 

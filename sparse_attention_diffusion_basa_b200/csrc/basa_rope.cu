@@ -16,10 +16,10 @@
 // its pairs, a token's angles are gathered once for all its heads, and rows come
 // by asynchronous copies that need no registers while they are under way.
 // Measured on a B200 (copy 6.57 TB/s), device time of the call: 128 x 128 grid, 24
-// heads of 128 in bf16, q, k, v slices of one projection 96.1 us = 6.28 TB/s (96% of
-// the copy rate); 21 x 45 x 80 clip, norm over 40 heads, q and k 503 us = 6.16 TB/s
-// (94%; the first form, unpacked and with an exchange between lanes a pair, 684);
-// backward of two 128 x 128 grids 260 us = 6.20 TB/s (94%; first form 389).
+// heads of 128 in bf16, q, k, v slices of one projection 93.3 us = 6.47 TB/s (98% of
+// the copy rate); 21 x 45 x 80 clip, norm over 40 heads, q and k 498 us = 6.22 TB/s
+// (95%; the first form, unpacked and with an exchange between lanes a pair, 684);
+// backward of two 128 x 128 grids 258 us = 6.25 TB/s (95%; first form 389).
 #include <math.h>
 #include <string.h>
 
@@ -346,7 +346,9 @@ template <typename T> constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
 // through a ring of asynchronous copies, private to each lane, that runs ahead
 // across tokens.  The norm's weight is folded into the angles:
 // A' = r (A (wA cos) - B (wB sin)).  Five CTAs an SM at 96 registers against
-// four at 128: 96 and 101 us for the 128 x 128 grid.
+// four at 128: 96 and 101 us for the 128 x 128 grid in bf16.  With a norm the fp32
+// forms spill there (8 bytes in the pairs layout, 24 in halves) and take 234 us, 79%
+// of the copy rate; bf16 in halves spills 8 bytes (95 us).
 template <typename TI, typename TO, int kLph, bool kHalves, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, 5)
     rope_head_kernel(const __grid_constant__ RopeArgs a) {
@@ -457,7 +459,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
 // Backward of rope_head_kernel, the same walk.  The weight's gradient is summed
 // in a lane's own sixteen columns over all its tokens and heads, then over the
 // CTA, and left as one row of partial sums a CTA.  Four CTAs an SM: 128 registers
-// hold the sums and a step without spills; two 128 x 128 grids with 24 heads 260 us.
+// hold the sums and a step without spills (fp32 in the pairs layout at 64 and 128
+// elements a head spills 8 bytes); two 128 x 128 grids with 24 heads 258 us.
 // Without a norm there are no sums: five CTAs, as forward (128 x 128 grid 96 us; four,
 // with the selects of what is not rotated, 100).
 template <typename T, int kLph, bool kHalves, bool kNorm>
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(512) rope_token_kernel(const __grid_constant__
 // Backward of rope_token_kernel.  Both sums of a row (x^2 and w gn x) share one
 // barrier; a thread's columns of the weight's gradient stay in registers over
 // all its tokens and are left as one row of partial sums a team.  Up to 5120
-// columns two CTAs of 320 threads share an SM without a spilled register (51 us
+// columns two CTAs of 320 threads share an SM without a spilled register (50 us
 // for a clip of 14508 tokens with 12 query and 4 K/V heads of 128, first form 99); up
 // to 8192 one CTA; beyond, 64 registers a thread and spills.  What bounds it there is
 // latency, not HBM (31.7 us): a barrier and two exchanges a token of 3 KB, and each
@@ -951,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   TokenAngles ang;
   ang.init(a, n, stride, tid, threads, sm);
-    ang.fetch(a, sm, 0, tid, threads);
+  ang.fetch(a, sm, 0, tid, threads);
   ang.fetch(a, sm, 1, tid, threads);
   copy_commit();
   f2 accA[4], accB[4];
