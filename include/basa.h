@@ -336,7 +336,8 @@ typedef struct basa_rope_params {
   int32_t at, ah, aw;  /* rotated elements of a head per axis: even, together at most d; the
                           rest of the head is not rotated (without a norm: copied).  Pairs
                           0 .. at/2 - 1 turn with the time coordinate, the next ah/2 with the
-                          row, the next aw/2 with the column.  BASA_ROPE_HALVES needs at + ah + aw a multiple of 16. */
+                          row, the next aw/2 with the column.  BASA_ROPE_HALVES needs
+                          at + ah + aw a multiple of 16. */
   int32_t layout;      /* BASA_ROPE_PAIRS or BASA_ROPE_HALVES */
   int32_t norm;        /* BASA_ROPE_NORM_*; _TOKEN takes H * d up to 16384 */
   float eps;           /* of the norm: positive */
