@@ -369,3 +369,48 @@ def test_border_backward_keeps_to_its_workspace(basa, rows, groups, C):
     t = t * (1 + mods[1].double()[:, None])
     ref, tol = t.sum((0, 1)), 140 * 2.0 ** -24 * t.abs().sum((0, 1))
     assert ((got.dbias.double() - ref).abs() <= tol + (ref.abs() + tol) * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("C", [264, 1536, 5120, 8192])
+@pytest.mark.parametrize("xt,yt", [(F32, BF), (F32, F32), (BF, BF)])
+def test_border_in_place_in_every_type(basa, xt, yt, C):
+    """x_out in x's place and h in y's, and the backward's dx in dx_out's (the C entry): the bits of a
+    call with outputs of its own, with more rows than are worked on at a time."""
+    from sparse_attention_diffusion_basa_b200 import _lib
+    x, y = rnd(1, 2, 1501, C, dtype=xt), rnd(2, 2, 1501, C, dtype=yt)
+    gate, scale = rnd(3, 2, C), rnd(4, 2, C)
+    kw = dict(gate=gate, scale=scale, post_norm="rms")
+    xo, h, st = basa.gated_norm(x, y, return_stats=True, **kw)
+    xc, yc = x.clone(), y.clone()
+    basa.gated_norm(xc, yc, x_out=xc, h_out=yc, **kw)
+    assert equal(xc, xo) and equal(yc, h)
+    gh, gx = rnd(5, 2, 1501, C, dtype=yt), rnd(6, 2, 1501, C, dtype=xt)
+    want = basa.gated_norm_bwd(gh, xo, st, y, gx, **kw)
+    t = lambda d: 0 if d == F32 else 1  # noqa: E731
+    prm = _lib.BasaGnormParams(3002, 2, C, 1, 2, 1e-6, 1e-6, 1.0, t(xt), t(yt), 0, 0, C, C, 0)
+    dy, dgate, dscale = torch.empty_like(y), torch.empty_like(gate), torch.empty_like(scale)
+    ws = torch.empty(_lib.load().basa_gated_norm_bwd_workspace_size(ctypes.byref(prm)), dtype=torch.uint8, device="cuda")
+    p = lambda a: a.data_ptr()  # noqa: E731
+    code = _lib.load().basa_gated_norm_bwd(p(gh), p(xo), p(st), p(y), p(gx), p(gate), None, None, None, p(scale), p(gx),
+                                           p(dy), p(dgate), None, None, None, p(dscale), None, p(ws),
+                                           ctypes.byref(prm), torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    for a, b in ((gx, want.dx), (dy, want.dy), (dgate, want.dgate), (dscale, want.dscale)):
+        assert equal(a, b)
+
+
+@pytest.mark.parametrize("norm,H,Hkv", [(None, 5, 5), ("head", 24, 8), ("token", 12, 3), ("token", 40, 40)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_preparation_in_place_over_many_tokens(basa, norm, H, Hkv, dtype):
+    """Every output in its input's place where rows are read ahead of those that are written."""
+    grid, axes = (3, 31, 47), (44, 42, 42)
+    table = basa.rope_table(grid, axes)
+    q, k, v = (rnd(i, 1, *grid, n, 128, dtype=dtype) for i, n in enumerate((H, Hkv, Hkv)))
+    want = basa.qkv_rope(q, k, v, table, axes, norm=norm)
+    place = [t.clone() for t in (q, k, v)]
+    basa.qkv_rope(*place, table, axes, norm=norm, out=place)
+    assert all(equal(a, b) for a, b in zip(place, want))
+    g = [rnd(5 + i, *t.shape, dtype=dtype) for i, t in enumerate((q, k, v))]
+    want = basa.qkv_rope_bwd(*g, q, k, table, axes, norm=norm)
+    basa.qkv_rope_bwd(*g, q, k, table, axes, norm=norm, out=g)
+    assert all(equal(a, b) for a, b in zip(g, want))
